@@ -495,6 +495,98 @@ rt_status rt_dequant_e4m3_f16(const uint8_t *Wq, uint16_t *W_out, int64_t N, int
                               void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 8-bit activations.  The cards quantize the weights only; these calls
+ * quantize the activations too, one scale a row (a token), so that a
+ * projection runs on the tensor cores' 8-bit instructions with nothing to
+ * dequantize.  The library's q8 and e4m3 weights are used as they are.
+ *
+ * An 8-bit row is K codes and one fp32 scale; its values are code * scale:
+ *   fmt RT_FMT_Q8    int8 codes, scale = max|v| / 127, code = v / scale rounded
+ *                    to nearest, ties to even: rt_quantize_q8_row's rule, and
+ *                    for fp32 input its bits, so device-made codes are q8
+ *                    weights too;
+ *   fmt RT_FMT_E4M3  float8_e4m3fn codes, scale = max|v| / 448, code = the
+ *                    e4m3 value nearest v / scale.
+ * A row of zeros has scale 0 and zero codes.  A row in which a value is
+ * infinite or NaN has scale NaN and zero codes, so the product makes that row
+ * of Y NaN and leaves the others alone; it latches RT_ERR_OPERAND_RANGE for
+ * rt_device_status().
+ *
+ * Conventions as for the GEMMs (ownership, device pointers on the current
+ * device, stream order, no exceptions), and:
+ *   - dtype is the element type of X, R, H, U, out or Y; values and sums are
+ *     fp32 inside, rounded once to dtype where they leave;
+ *   - all tensors are row-major and contiguous; K (F) is a multiple of 16 and
+ *     at most 32768 for the calls that make 8-bit rows, 131056 for the product
+ *     and rt_dequant_a8 (RT_ERR_UNSUPPORTED_SHAPE): a row stays in one
+ *     block's registers, and the int8 product's sum in int32;
+ *   - X, R, H, U, out, codes, Xq, Wq, Y and gain 16-byte aligned, scales and
+ *     bias 4-byte aligned (RT_ERR_ALIGNMENT);
+ *   - 0 <= M, 1 <= N, both below 2^31 - 1023; M == 0 is a no-op;
+ *   - outputs overlap no input and no other output (RT_ERR_INVALID_ARG);
+ *     rt_addnorm_a8's H may be X or R itself;
+ *   - no call allocates or needs a workspace, so all of them can be captured
+ *     into a CUDA graph as they are, and calls on different streams share
+ *     nothing.
+ */
+typedef enum rt_dtype {
+    RT_DTYPE_F32 = 0,
+    RT_DTYPE_F16 = 1,
+    RT_DTYPE_BF16 = 2
+} rt_dtype;
+
+/* X [M, K] -> codes [M, K] (int8 or uint8 e4m3), scales [M]. */
+rt_status rt_quantize_a8(int fmt, int dtype, const void *X, void *codes, float *scales, int64_t M,
+                         int64_t K, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, into 8 bits:
+ *   h = X + R (R NULL: h = X),  H = h rounded to dtype (H NULL: not stored),
+ *   y = h / sqrt(mean_k h^2 + eps) * gain (gain fp32 [K]; NULL: all ones),
+ *   codes, scales = y in 8 bits.
+ * The norm is of the fp32 sum h, not of the rounded H.  eps must be a finite
+ * normal positive number (RT_ERR_INVALID_ARG).
+ */
+rt_status rt_addnorm_a8(int fmt, int dtype, const void *X, const void *R, const float *gain,
+                        float eps, void *H, void *codes, float *scales, int64_t M, int64_t K,
+                        void *stream);
+
+/*
+ * Gated SiLU into 8 bits: U [M, 2F] holds a | b (the rows a w1|w3 projection
+ * gives), y = a * sigmoid(a) * b, codes [M, F], scales [M] = y in 8 bits.
+ */
+rt_status rt_gate_a8(int fmt, int dtype, const void *U, void *codes, float *scales, int64_t M,
+                     int64_t F, void *stream);
+
+/* out [M, K] = code * scale, one rounding to dtype. */
+rt_status rt_dequant_a8(int fmt, int dtype, const void *codes, const float *scales, void *out,
+                        int64_t M, int64_t K, void *stream);
+
+/*
+ * Product of 8-bit activations and 8-bit weights of the same format:
+ *   Y[m, o] = (sum_k Xq[m, k] * Wq[o, k]) * w_scales[o] * x_scales[m] + bias[o]
+ *   Xq [M, K], x_scales [M]; Wq [N, K], w_scales [N]: the q8 weight of
+ *   rt_qgemm_q8, or an e4m3 weight with row scales or, as rt_gemm_e4m3's,
+ *   without (NULL); bias fp32 [N] or NULL; Y [M, N] of dtype.
+ * The int8 sum is exact (int32) and is rounded to fp32 once; the e4m3 sum is
+ * fp32.  tcgen05 kernels for every M: K split over clusters where there are
+ * few tiles, persistent tiles otherwise, on CTA pairs where those are faster.
+ * A row's int8 result does not depend on the call's other rows; an e4m3 row's
+ * depends on them only through the plan, which fixes the order of the sum.  An
+ * output that is not finite in dtype latches RT_ERR_OPERAND_RANGE.
+ */
+rt_status rt_qgemm_a8(int fmt, int dtype, const void *Xq, const float *x_scales, const void *Wq,
+                      const float *w_scales, const float *bias, void *Y, int64_t M, int64_t N,
+                      int64_t K, void *stream);
+
+/* How rt_qgemm_a8 tiles this product on the current device: *tile_rows
+ * activation rows and *split CTAs to a tile; returns 1 where CTA pairs share an
+ * MMA over 256 weight rows, 0 for 128 weight rows to a CTA, -1 for sizes the
+ * product refuses.  Without a device, the plan for 148 SMs. */
+int rt_qgemm_a8_plan(int64_t M, int64_t N, int64_t K, int *tile_rows, int *split);
+
+/*
  * Synchronizes `stream`, then reads and clears the current device's status
  * word, which the tensor-core kernels latch when one of their bounded waits
  * gives up (RT_ERR_DEVICE_TIMEOUT; outputs of that launch are undefined) or

@@ -25,7 +25,8 @@ __all__ = [
     "qgemm_batch", "batch_plan", "Proj", "QBlockFmt", "qblock_project_fmt", "block_fused_fmt",
     "gemm_e4m3", "quantize_e4m3", "dequant_e4m3_f32", "dequant_e4m3_f16", "FMT_E4M3",
     "Checkpoint", "qgemm", "block_route", "ROUTE_GROUPED_SMALL_M", "ROUTE_X_RESIDENT_GROUP",
-    "ROUTE_SIDE_PREPASS",
+    "ROUTE_SIDE_PREPASS", "FMT_Q4", "FMT_Q8", "quantize_a8", "addnorm_a8", "gate_a8", "dequant_a8",
+    "qgemm_a8", "a8_plan",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -153,6 +154,18 @@ def lib() -> ctypes.CDLL:
     L.rt_qgemm_batch.argtypes = [ctypes.POINTER(_QProjC), _i32, _i64, _i32, _p]
     L.rt_qgemm_batch_plan.restype = _i32
     L.rt_qgemm_batch_plan.argtypes = [ctypes.POINTER(_QProjC), _i32, _i64, _i32]
+    L.rt_quantize_a8.restype = _i32
+    L.rt_quantize_a8.argtypes = [_i32, _i32, _p, _p, _p, _i64, _i64, _p]
+    L.rt_addnorm_a8.restype = _i32
+    L.rt_addnorm_a8.argtypes = [_i32, _i32, _p, _p, _p, ctypes.c_float, _p, _p, _p, _i64, _i64, _p]
+    L.rt_gate_a8.restype = _i32
+    L.rt_gate_a8.argtypes = [_i32, _i32, _p, _p, _p, _i64, _i64, _p]
+    L.rt_dequant_a8.restype = _i32
+    L.rt_dequant_a8.argtypes = [_i32, _i32, _p, _p, _p, _i64, _i64, _p]
+    L.rt_qgemm_a8.restype = _i32
+    L.rt_qgemm_a8.argtypes = [_i32, _i32, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]
+    L.rt_qgemm_a8_plan.restype = _i32
+    L.rt_qgemm_a8_plan.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
     _lib = L
     return L
 
@@ -281,6 +294,30 @@ def rt_workspace_reserve(nbytes, stream) -> int:
 
 def rt_workspace_release() -> int:
     return lib().rt_workspace_release()
+
+
+def rt_quantize_a8(fmt, dtype, X, codes, scales, M, K, stream) -> int:
+    return lib().rt_quantize_a8(fmt, dtype, X, codes, scales, M, K, stream)
+
+
+def rt_addnorm_a8(fmt, dtype, X, R, gain, eps, H, codes, scales, M, K, stream) -> int:
+    return lib().rt_addnorm_a8(fmt, dtype, X, R, gain, eps, H, codes, scales, M, K, stream)
+
+
+def rt_gate_a8(fmt, dtype, U, codes, scales, M, F, stream) -> int:
+    return lib().rt_gate_a8(fmt, dtype, U, codes, scales, M, F, stream)
+
+
+def rt_dequant_a8(fmt, dtype, codes, scales, out, M, K, stream) -> int:
+    return lib().rt_dequant_a8(fmt, dtype, codes, scales, out, M, K, stream)
+
+
+def rt_qgemm_a8(fmt, dtype, Xq, x_scales, Wq, w_scales, bias, Y, M, N, K, stream) -> int:
+    return lib().rt_qgemm_a8(fmt, dtype, Xq, x_scales, Wq, w_scales, bias, Y, M, N, K, stream)
+
+
+def rt_qgemm_a8_plan(M, N, K, tile_rows, split) -> int:
+    return lib().rt_qgemm_a8_plan(M, N, K, tile_rows, split)
 
 
 # ------------------------------------------------------- torch-level helpers
@@ -420,6 +457,214 @@ def qgemm_noalloc(fmt, X, Wq, scales, Y, path="auto", stream=None):
                           M, N, K, _path(path), _stream_ptr(stream))
     _check(st, "rt_qgemm_noalloc")
     return Y
+
+
+# ---------------------------------------------------------- 8-bit activations
+# These calls run a few microseconds on the GPU, so their checks are one
+# expression an operand (about 0.3 us); only a refused operand is looked at
+# again, for the message.
+_a8_state = None
+
+
+def _a8():
+    """(rt_dtype of each torch dtype, codes dtype of each format, float32,
+    current raw stream of a device index, current device index)."""
+    global _a8_state
+    if _a8_state is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(index):
+                return torch.cuda.current_stream(index).cuda_stream
+        current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _a8_state = ({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2},
+                     {FMT_Q8: torch.int8, FMT_E4M3: torch.uint8}, torch.float32, raw, current)
+    return _a8_state
+
+
+def _a8_refuse(t, dtype, shape, name, index):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{index}")
+
+
+def _a8_ptr(t, dtype, shape, name, index):
+    """Pointer of one operand: type, shape, layout and device checked."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _a8_refuse(t, dtype, shape, name, index)
+
+
+def _a8_first(t, types, name):
+    """(rt_dtype, rows, columns, device index) of a call's first operand."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be {' or '.join(map(str, types))}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    return code, rows, cols, t.get_device()
+
+
+def _a8_codes(fmt, codes):
+    try:
+        return codes[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"fmt must be 8 (q8) or 3 (e4m3), got {fmt}") from None
+
+
+def _a8_stream(stream, index, raw, current):
+    """Stream handle; the library launches on the current device, so operands
+    of another device, or a stream of another one, are refused."""
+    if current() != index:
+        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{current()}")
+    if stream is None:
+        return raw(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _a8_new(shape, dtype, index):
+    import torch
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+
+
+def quantize_a8(X, fmt=FMT_Q8, codes=None, scales=None, stream=None):
+    """(codes, scales) of the rows of X [M, K] in 8 bits: int8 (fmt 8) or
+    e4m3 (fmt 3, as uint8), X float32, float16 or bfloat16."""
+    types, cdts, f32, raw, current = _a8()
+    cdt = _a8_codes(fmt, cdts)
+    dt, M, K, dev = _a8_first(X, types, "X")
+    if codes is None:
+        codes = _a8_new((M, K), cdt, dev)
+    if scales is None:
+        scales = _a8_new((M,), f32, dev)
+    st = rt_quantize_a8(fmt, dt, _a8_ptr(X, X.dtype, (M, K), "X", dev),
+                        _a8_ptr(codes, cdt, (M, K), "codes", dev),
+                        _a8_ptr(scales, f32, (M,), "scales", dev), M, K,
+                        _a8_stream(stream, dev, raw, current))
+    if st:
+        _check(st, "rt_quantize_a8")
+    return codes, scales
+
+
+def addnorm_a8(X, gain=None, fmt=FMT_Q8, residual=None, eps=1e-6, H=None, codes=None, scales=None,
+               stream=None):
+    """(codes, scales, H): the root-mean-square norm of h = X + residual, times
+    gain (fp32 [K] or None), in 8 bits, and h in X's type.  Without a residual
+    h is X, and H (None unless given) is only written if given.  H may be X or
+    residual itself."""
+    types, cdts, f32, raw, current = _a8()
+    cdt = _a8_codes(fmt, cdts)
+    dt, M, K, dev = _a8_first(X, types, "X")
+    xdt, shape = X.dtype, (M, K)
+    if residual is not None and H is None:
+        H = _a8_new(shape, xdt, dev)
+    if codes is None:
+        codes = _a8_new(shape, cdt, dev)
+    if scales is None:
+        scales = _a8_new((M,), f32, dev)
+    st = rt_addnorm_a8(fmt, dt, _a8_ptr(X, xdt, shape, "X", dev),
+                       None if residual is None else _a8_ptr(residual, xdt, shape, "residual", dev),
+                       None if gain is None else _a8_ptr(gain, f32, (K,), "gain", dev), eps,
+                       None if H is None else _a8_ptr(H, xdt, shape, "H", dev),
+                       _a8_ptr(codes, cdt, shape, "codes", dev),
+                       _a8_ptr(scales, f32, (M,), "scales", dev), M, K,
+                       _a8_stream(stream, dev, raw, current))
+    if st:
+        _check(st, "rt_addnorm_a8")
+    return codes, scales, H
+
+
+def gate_a8(U, fmt=FMT_Q8, codes=None, scales=None, stream=None):
+    """(codes, scales) of silu(a) * b in 8 bits, U [M, 2F] = a | b."""
+    types, cdts, f32, raw, current = _a8()
+    cdt = _a8_codes(fmt, cdts)
+    dt, M, F2, dev = _a8_first(U, types, "U")
+    if F2 % 2:
+        raise ValueError(f"U must hold two halves, got {F2} columns")
+    F = F2 // 2
+    if codes is None:
+        codes = _a8_new((M, F), cdt, dev)
+    if scales is None:
+        scales = _a8_new((M,), f32, dev)
+    st = rt_gate_a8(fmt, dt, _a8_ptr(U, U.dtype, (M, F2), "U", dev),
+                    _a8_ptr(codes, cdt, (M, F), "codes", dev),
+                    _a8_ptr(scales, f32, (M,), "scales", dev), M, F,
+                    _a8_stream(stream, dev, raw, current))
+    if st:
+        _check(st, "rt_gate_a8")
+    return codes, scales
+
+
+def dequant_a8(fmt, codes, scales, dtype=None, out=None, stream=None):
+    """The values code * scale [M, K] in dtype (of out where given, else bfloat16)."""
+    types, cdts, f32, raw, current = _a8()
+    cdt = _a8_codes(fmt, cdts)
+    _, M, K, dev = _a8_first(codes, {cdt: 0}, "codes")
+    if out is None:
+        import torch
+        out = _a8_new((M, K), dtype or torch.bfloat16, dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
+    dt = _a8_first(out, types, "out")[0]
+    st = rt_dequant_a8(fmt, dt, _a8_ptr(codes, cdt, (M, K), "codes", dev),
+                       _a8_ptr(scales, f32, (M,), "scales", dev),
+                       _a8_ptr(out, out.dtype, (M, K), "out", dev), M, K,
+                       _a8_stream(stream, dev, raw, current))
+    if st:
+        _check(st, "rt_dequant_a8")
+    return out
+
+
+def qgemm_a8(fmt, Xq, x_scales, Wq, w_scales=None, bias=None, Y=None, dtype=None, stream=None):
+    """Y [M, N] = (Xq [M, K] @ Wq [N, K]^T) * x_scales [M, 1] * w_scales [1, N] +
+    bias [N], both operands int8 (fmt 8) or e4m3 (fmt 3; w_scales may be None).
+    Y's type is dtype, or that of Y where given, else float32."""
+    types, cdts, f32, raw, current = _a8()
+    cdt = _a8_codes(fmt, cdts)
+    _, M, K, dev = _a8_first(Xq, {cdt: 0}, "Xq")
+    _, N, _, _ = _a8_first(Wq, {cdt: 0}, "Wq")
+    if fmt == FMT_Q8 and w_scales is None:
+        raise TypeError("q8 weights have row scales")
+    if Y is None:
+        Y = _a8_new((M, N), dtype or f32, dev)
+    elif dtype is not None and Y.dtype != dtype:
+        raise TypeError(f"Y is {Y.dtype}, dtype {dtype}")
+    dt = _a8_first(Y, types, "Y")[0]
+    st = rt_qgemm_a8(fmt, dt, _a8_ptr(Xq, cdt, (M, K), "Xq", dev),
+                     _a8_ptr(x_scales, f32, (M,), "x_scales", dev),
+                     _a8_ptr(Wq, cdt, (N, K), "Wq", dev),
+                     None if w_scales is None else _a8_ptr(w_scales, f32, (N,), "w_scales", dev),
+                     None if bias is None else _a8_ptr(bias, f32, (N,), "bias", dev),
+                     _a8_ptr(Y, Y.dtype, (M, N), "Y", dev), M, N, K,
+                     _a8_stream(stream, dev, raw, current))
+    if st:
+        _check(st, "rt_qgemm_a8")
+    return Y
+
+
+def a8_plan(M, N, K):
+    """How qgemm_a8 tiles these sizes on the current device: a dict of `rows`
+    (activation rows a tile), `split` (CTAs that share a tile's K) and `pair`
+    (CTA pairs share an MMA); None for sizes it refuses."""
+    rows, split = _i32(), _i32()
+    r = rt_qgemm_a8_plan(M, N, K, ctypes.byref(rows), ctypes.byref(split))
+    return None if r < 0 else {"rows": rows.value, "split": split.value, "pair": bool(r)}
 
 
 @dataclass

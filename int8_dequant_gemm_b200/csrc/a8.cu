@@ -1,0 +1,561 @@
+// Product of 8-bit activations and 8-bit weights on the tensor cores' 8-bit
+// instructions:
+//
+//   Y[m, o] = (sum_k Xc[m, k] * Wc[o, k]) * ws[o] * xs[m] + bias[o]
+//
+// with int8 codes (tcgen05.mma kind::i8, the sum exact in int32) or FP8 E4M3
+// codes (kind::f8f6f4, fp32 sum).  The scales leave the sum because each is
+// constant along k, so nothing is dequantized and both operands go from HBM to
+// the tensor core as they are stored: TMA boxes of 128 bytes of K in the
+// 128-byte-swizzled operand layout.
+//
+// Orientation as in the other tensor-core kernels: weight rows are the MMA's M
+// (TMEM lanes), activation rows its N (TMEM columns).  A warp of the epilogue
+// then holds 32 consecutive outputs of one Y row, so plain stores are whole
+// 128-byte segments of Y for every N and alignment.
+//
+// Roles (12 warps): warp 0 TMA, warp 1 MMA issue, warps 4-11 epilogue (two per
+// TMEM lane quadrant, alternating 16-column chunks); warps 2-3 idle.
+//
+// Three shapes of the same code:
+//   - persistent tiles of 128 weight rows x bn activation rows, one CTA each,
+//     two accumulators so that a tile's epilogue runs under the next one's MMAs;
+//   - the same on CTA pairs (PAIR): one cta_group::2 MMA over 256 weight rows,
+//     each CTA staging its own 128 weight rows and half of the activation rows;
+//   - few tiles: K split over a cluster of `split` CTAs, one tile a cluster,
+//     partial sums added in rank order through distributed shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "kernels.cuh"
+#include "tmapipe.cuh"
+
+namespace rtq {
+namespace {
+
+constexpr int kKBytes = 128;                       // K per stage: one swizzled row
+constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights a stage
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;   // 384
+constexpr int kMaxBn = 256, kMaxStages = 8;
+constexpr int kBand = 8;                           // activation tiles walked together
+constexpr uint32_t kEpiBar = 1;                    // named barrier of the epilogue warps
+constexpr uint16_t kBoth = 3;                      // multicast mask: both CTAs of a pair
+constexpr int kSmemMax = 200 * 1024;               // ring of stages
+
+struct A8Args {
+    const float *xs, *ws, *bias;
+    void *Y;
+    int M, N, K, bn, stages, split, n_o, n_m, acc_cols;
+};
+
+__host__ __device__ constexpr int stage_bytes(int bn, int pair) {
+    return kABytes + (pair ? bn / 2 : bn) * kKBytes;
+}
+
+// Ring, then xs[2][kMaxBn], then the barriers and words below.
+__host__ __device__ inline int tail_offset(const A8Args &a, int pair) {
+    const int ring = a.stages * stage_bytes(a.bn, pair);
+    const int red = a.split > 1 ? a.bn * kTileRows * 4 : 0;   // partial sums reuse the ring
+    return ring > red ? ring : red;
+}
+constexpr int kTailBytes = 2 * kMaxBn * 4 + (2 * kMaxStages + 5) * 8 + 16;
+
+// Instruction descriptors (A and B K-major): accumulator s32 (2) or f32 (1),
+// operand type 1 = s8 of kind::i8, 0 = e4m3 of kind::f8f6f4.
+__host__ __device__ constexpr uint32_t idesc_8bit(int fmt, int M, int N) {
+    return ((fmt == kFmtQ8 ? 2u : 1u) << 4) | ((fmt == kFmtQ8 ? 1u : 0u) << 7) |
+           ((fmt == kFmtQ8 ? 1u : 0u) << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+#define RTQ_MMA8(group, kind)                                                   \
+    asm volatile(                                                               \
+        "{\n\t.reg .pred p;\n\t"                                                \
+        "setp.ne.b32 p, %4, 0;\n\t"                                             \
+        "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" \
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                   \
+        : "memory")
+    if (FMT == kFmtQ8) {
+        if (PAIR) RTQ_MMA8("2", "i8");
+        else RTQ_MMA8("1", "i8");
+    } else {
+        if (PAIR) RTQ_MMA8("2", "f8f6f4");
+        else RTQ_MMA8("1", "f8f6f4");
+    }
+#undef RTQ_MMA8
+}
+
+// TMA load of a CTA of a pair: into this CTA's shared memory, its bytes
+// counted on the mbarrier at `cbar` (a shared::cluster address in either CTA).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                                 uint32_t cbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cbar)
+        : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ float acc_f32(uint32_t v) {
+    return FMT == kFmtQ8 ? __int2float_rn(static_cast<int>(v)) : __uint_as_float(v);
+}
+
+__device__ __forceinline__ float to_type(float v, const float *) { return v; }
+__device__ __forceinline__ __half to_type(float v, const __half *) { return __float2half_rn(v); }
+__device__ __forceinline__ __nv_bfloat16 to_type(float v, const __nv_bfloat16 *) {
+    return __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Tile t of the walk: bands of kBand activation tiles, all weight tiles of a
+// band, activation tile fastest.  The tiles that run at once then share few
+// operand rows, which stay in L2.
+struct TileAt {
+    int m, o;
+    __device__ TileAt(int t, int n_m, int n_o) {
+        const int band = t / (kBand * n_o);
+        const int m0 = band * kBand, mb = min(kBand, n_m - m0);
+        const int r = t - band * kBand * n_o;
+        m = m0 + r % mb;
+        o = r / mb;
+    }
+};
+
+template <int FMT, typename YT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    a8_qgemm_kernel(const __grid_constant__ CUtensorMap x_map,
+                    const __grid_constant__ CUtensorMap w_map, const A8Args a, DevCtl *ctl) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = smem_addr(smem);
+    uint8_t *tail = smem + tail_offset(a, PAIR);
+    float *xs_s = reinterpret_cast<float *>(tail);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 2 * kMaxBn * 4);
+    uint64_t *empty = full + kMaxStages;
+    uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile uint32_t *failed = tmem_slot + 1;     // split: this rank has no sum
+
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    const int split = PAIR ? 1 : a.split;
+    const int csize = PAIR ? 2 : split;
+    const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool leader = !PAIR || rank == 0;
+    const int nkb = (a.K + kKBytes - 1) / kKBytes;
+    const int kb0 = nkb * (PAIR ? 0 : rank) / split, kb1 = nkb * ((PAIR ? 0 : rank) + 1) / split;
+    const int n_tiles = a.n_o * a.n_m;
+    const int first = static_cast<int>(blockIdx.x) / csize;
+    const int step = static_cast<int>(gridDim.x) / csize;
+    const int sbytes = stage_bytes(a.bn, PAIR);
+    const unsigned long long *lim = &ctl->wait_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *failed = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tmem_alloc_pair(tmem_slot, static_cast<uint32_t>(a.acc_cols));
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, static_cast<uint32_t>(a.acc_cols));
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (PAIR) cluster_sync();      // the peer's barriers are initialised
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    // Every operand, the weights and scales too, may be the previous kernel's
+    // output.  Dependents are released only after that kernel is complete, so
+    // one that reads ahead of its own wait reads nothing older than this grid.
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    bool ok = true;
+
+    if (warp == 0) {
+        // ============================================================ TMA
+        // (Test hook: with `inject` the first weight box is never requested.)
+        if (lane == 0) {
+            int s = 0, j = 0;
+            uint32_t par = 1;
+            const uint32_t xb = static_cast<uint32_t>(sbytes - kABytes);
+            for (int t = first; t < n_tiles && ok; t += step) {
+                const TileAt at(t, a.n_m, a.n_o);
+                const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
+                const int my = at.m * a.bn + (PAIR ? rank * (a.bn / 2) : 0);
+                for (int kb = kb0; kb < kb1; ++kb, ++j) {
+                    if (j >= a.stages && !mbar_wait(&empty[s], par, lim)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool skip = j == 0 && leader && ctl->inject;
+                    const uint32_t dst = base + static_cast<uint32_t>(s * sbytes);
+                    if (PAIR) {
+                        const uint32_t cbar = cluster_map(smem_addr(&full[s]), 0);
+                        if (leader) mbar_expect_tx(&full[s], 2u * static_cast<uint32_t>(sbytes));
+                        if (!skip) tma_load_2d_pair(dst, &w_map, kb * kKBytes, oy, cbar);
+                        tma_load_2d_pair(dst + kABytes, &x_map, kb * kKBytes, my, cbar);
+                    } else {
+                        mbar_expect_tx(&full[s], kABytes + xb);
+                        if (!skip) tma_load_2d(dst, &w_map, kb * kKBytes, oy, &full[s]);
+                        tma_load_2d(dst + kABytes, &x_map, kb * kKBytes, my, &full[s]);
+                    }
+                    if (++s == a.stages) {
+                        s = 0;
+                        par ^= 1;
+                    }
+                }
+            }
+            // Before the CTA may exit, every box it requested has landed
+            // (immediate unless a consumer gave up; a pair's boxes are counted
+            // by its even CTA, which the odd one meets before it exits).
+            if (leader) {
+                for (int i = 0; i < a.stages && i < j; ++i) {
+                    const int last_j = i + ((j - 1 - i) / a.stages) * a.stages;
+                    if (!(last_j == 0 && ctl->inject))
+                        mbar_wait(&full[i], static_cast<uint32_t>(last_j / a.stages) & 1u, lim);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ============================================================ MMA issue
+        if (leader) {
+            const uint32_t idesc = idesc_8bit(FMT, (PAIR ? 2 : 1) * kTileRows, a.bn);
+            int s = 0, n_local = 0;
+            uint32_t par = 0;
+            for (int t = first; t < n_tiles && ok; t += step, ++n_local) {
+                const int b = n_local & 1;
+                if (n_local >= 2)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&acc_empty[b],
+                                              static_cast<uint32_t>((n_local / 2) - 1) & 1u, lim));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem + static_cast<uint32_t>(b * a.bn);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full[s], par, lim));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t st = base + static_cast<uint32_t>(s * sbytes);
+                    const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
+                    const int left = a.K - kb * kKBytes;       // 32 K a step; rest is zero fill
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (kk * 32 < left)
+                                mma_8bit<FMT, PAIR>(d, ad + 2 * kk, bd + 2 * kk, idesc,
+                                                    (kb > kb0 || kk > 0) ? 1u : 0u);
+                        if (PAIR) tc_commit_pair_mc(&empty[s], kBoth);
+                        else tc_commit(&empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == a.stages) {
+                        s = 0;
+                        par ^= 1;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if (PAIR) tc_commit_pair_mc(&acc_full[b], kBoth);
+                    else tc_commit(&acc_full[b]);
+                }
+                __syncwarp();
+            }
+            if (!ok) {                       // issued MMAs end before the CTA does
+                if (elect_one()) {
+                    if (PAIR) tc_commit_pair_mc(drain, 1);
+                    else tc_commit(drain);
+                    mbar_wait(drain, 0, lim);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ============================================================ epilogue
+        const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+        const int et = static_cast<int>(threadIdx.x) - kEpiWarp0 * 32;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        YT *const Y = static_cast<YT *>(a.Y);
+        float nf = 0.f;                      // NaN once an output is not finite
+        int n_local = 0;
+        for (int t = first; t < n_tiles && ok; t += step, ++n_local) {
+            const TileAt at(t, a.n_m, a.n_o);
+            const int b = n_local & 1;
+            const int m0 = at.m * a.bn;
+            const int mlim = min(a.bn, a.M - m0);
+            if (split > 1) {
+                // partial sums into this CTA's shared memory, [column][lane]
+                ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, lim));
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t *red = reinterpret_cast<uint32_t *>(smem);
+                for (int c = 16 * h; c < a.bn; c += 32) {
+                    uint32_t v[16];
+                    tmem_ld_x16(tq + static_cast<uint32_t>(c), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        red[(c + i) * kTileRows + q * 32 + lane] = v[i];
+                }
+                tc_fence_before_sync();
+                continue;
+            }
+            float *xs_t = xs_s + b * kMaxBn;
+            xs_t[et] = et < mlim ? __ldg(a.xs + m0 + et) : 0.f;
+            const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
+            const bool live = o < a.N;
+            const float wsc = live && a.ws ? __ldg(a.ws + o) : 1.f;
+            const float bo = live && a.bias ? __ldg(a.bias + o) : 0.f;
+            named_bar_sync(kEpiBar, kEpiThreads);
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&acc_full[b], static_cast<uint32_t>(n_local / 2) & 1u, lim));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t tb = tq + static_cast<uint32_t>(b * a.bn);
+            YT *yo = Y + static_cast<size_t>(m0) * a.N + o;
+            for (int c = 16 * h; c < a.bn; c += 32) {
+                uint32_t v[16];
+                tmem_ld_x16(tb + static_cast<uint32_t>(c), v);
+                tmem_ld_wait();
+                const int n = live ? min(16, mlim - c) : 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (i < n) {
+                        const YT y = to_type(fmaf(acc_f32<FMT>(v[i]) * wsc, xs_t[c + i], bo), Y);
+                        nf = fmaf(to_f32(y), 0.f, nf);
+                        yo[static_cast<size_t>(c + i) * a.N] = y;
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_remote(cluster_map(smem_addr(&acc_empty[b]), 0));
+                else mbar_arrive(&acc_empty[b]);
+            }
+        }
+        if (__any_sync(0xffffffffu, nf != 0.f) && lane == 0)
+            atomicOr(&ctl->status, 1u << kStatusRange);
+    }
+    if (!ok) {
+        atomicOr(&ctl->status, 1u << kStatusTimeout);
+        *failed = 1;
+    }
+    tc_fence_before_sync();
+    if (csize > 1) cluster_sync();
+    else __syncthreads();
+    if (!PAIR && split > 1) {
+        // ============================================================ split-K sum
+        // Rank r of the cluster adds and stores columns [bn r / split,
+        // bn (r + 1) / split) of all ranks' partial sums, in rank order.
+        bool all = true;
+        for (int r = 0; r < split; ++r)
+            all = all && ld_cluster_u32(cluster_map(smem_addr(const_cast<uint32_t *>(failed)),
+                                                    static_cast<uint32_t>(r))) == 0;
+        if (warp >= kEpiWarp0 && all) {
+            const TileAt at(first, a.n_m, a.n_o);
+            YT *const Y = static_cast<YT *>(a.Y);
+            float nf = 0.f;
+            const int m0 = at.m * a.bn;
+            const int c1 = min(a.bn * (rank + 1) / split, a.M - m0);
+            const int o = at.o * kTileRows + 4 * lane;
+            float wsc[4], bo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wsc[i] = o + i < a.N && a.ws ? __ldg(a.ws + o + i) : 1.f;
+                bo[i] = o + i < a.N && a.bias ? __ldg(a.bias + o + i) : 0.f;
+            }
+            for (int c = a.bn * rank / split + warp - kEpiWarp0; c < c1; c += kEpiWarps) {
+                const float xv = __ldg(a.xs + m0 + c);
+                const uint32_t at_c = base + static_cast<uint32_t>((c * kTileRows + 4 * lane) * 4);
+                float4 p[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < split) p[r] = ld_cluster_f4(cluster_map(at_c, static_cast<uint32_t>(r)));
+                float sf[4] = {0.f, 0.f, 0.f, 0.f};
+                int si[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < split) {
+                        const float e[4] = {p[r].x, p[r].y, p[r].z, p[r].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (FMT == kFmtQ8) si[i] += __float_as_int(e[i]);
+                            else sf[i] += e[i];
+                        }
+                    }
+                YT *yo = Y + static_cast<size_t>(m0 + c) * a.N + o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (o + i < a.N) {
+                        const float s = FMT == kFmtQ8 ? __int2float_rn(si[i]) : sf[i];
+                        const YT y = to_type(fmaf(s * wsc[i], xv, bo[i]), Y);
+                        nf = fmaf(to_f32(y), 0.f, nf);
+                        yo[i] = y;
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, nf != 0.f) && lane == 0)
+                atomicOr(&ctl->status, 1u << kStatusRange);
+        }
+        __syncwarp();
+        cluster_sync();                      // no rank exits while another reads its sums
+    }
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if (PAIR) tmem_dealloc_pair(tmem, static_cast<uint32_t>(a.acc_cols));
+        else tmem_dealloc(tmem, static_cast<uint32_t>(a.acc_cols));
+    }
+}
+
+template <int FMT, typename YT, bool PAIR>
+cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const void *Wq,
+                      const float *wsc, const float *bias, void *Y, int M, int N, int K,
+                      DevCtl *ctl, cudaStream_t st) {
+    static std::atomic<bool> attr_done[kMaxDevices];
+    static std::atomic<int> pairs_cache[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = smem_attr_once(a8_qgemm_kernel<FMT, YT, PAIR>, 227 * 1024, dev, attr_done)) !=
+        cudaSuccess)
+        return e;
+    A8Args a = {};
+    a.xs = xs;
+    a.ws = wsc;
+    a.bias = bias;
+    a.Y = Y;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bn = plan.bn;
+    a.split = PAIR ? 1 : plan.split;
+    const int nkb = (K + kKBytes - 1) / kKBytes;
+    const int ot = PAIR ? 2 * kTileRows : kTileRows;
+    a.n_o = (N + ot - 1) / ot;
+    a.n_m = (M + a.bn - 1) / a.bn;
+    a.stages = std::min(kMaxStages, kSmemMax / stage_bytes(a.bn, PAIR));
+    const int64_t tiles = static_cast<int64_t>(a.n_o) * a.n_m;
+    if (tiles > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    if (a.split > 1) a.stages = std::min(a.stages, (nkb + a.split - 1) / a.split);
+    int acc = 32;
+    while (acc < (a.split > 1 ? 1 : 2) * a.bn) acc *= 2;
+    a.acc_cols = acc;
+
+    CUtensorMap x_map, w_map;
+    if (!encode_tma_2d(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Xq, K, M, kKBytes,
+                       CU_TENSOR_MAP_SWIZZLE_128B, PAIR ? a.bn / 2 : a.bn) ||
+        !encode_tma_2d(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Wq, K, N, kKBytes,
+                       CU_TENSOR_MAP_SWIZZLE_128B, kTileRows))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = tail_offset(a, PAIR) + kTailBytes + 1024;
+    cfg.stream = st;
+    int grid;
+    if (PAIR) {
+        // the clusters' shared memory barely depends on the plan: one count serves all
+        cudaLaunchConfig_t most = cfg;
+        most.dynamicSmemBytes = kSmemMax + kTailBytes + 1024;
+        grid = 2 * static_cast<int>(std::min<int64_t>(
+                       tiles, resident_pairs(a8_qgemm_kernel<FMT, YT, PAIR>, most, dev, pairs_cache)));
+    } else {
+        grid = a.split > 1 ? static_cast<int>(tiles) * a.split
+                           : static_cast<int>(std::min<int64_t>(tiles, sm_count()));
+    }
+    cfg.gridDim = dim3(grid, 1, 1);
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    const int csize = PAIR ? 2 : a.split;
+    if (csize > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = csize;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, a8_qgemm_kernel<FMT, YT, PAIR>, x_map, w_map, a, ctl);
+}
+
+template <int FMT, typename YT>
+cudaError_t launch_a8_p(const A8Plan &p, const void *Xq, const float *xs, const void *Wq,
+                        const float *wsc, const float *bias, void *Y, int M, int N, int K,
+                        DevCtl *ctl, cudaStream_t s) {
+    return p.pair ? launch_a8<FMT, YT, true>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s)
+                  : launch_a8<FMT, YT, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+}
+
+template <int FMT>
+cudaError_t launch_a8_y(const A8Plan &p, int dtype, const void *Xq, const float *xs, const void *Wq,
+                        const float *wsc, const float *bias, void *Y, int M, int N, int K,
+                        DevCtl *ctl, cudaStream_t s) {
+    if (dtype == RT_DTYPE_F32)
+        return launch_a8_p<FMT, float>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    if (dtype == RT_DTYPE_F16)
+        return launch_a8_p<FMT, __half>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    return launch_a8_p<FMT, __nv_bfloat16>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+}
+
+}  // namespace
+
+int sm_count() {
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return n;
+    }
+    const int known = cache[dev].load(std::memory_order_acquire);
+    if (known > 0) return known;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    cache[dev].store(n, std::memory_order_release);
+    return n;
+}
+
+A8Plan plan_a8(int M, int N, int K, int sms) {
+    const int nkb = (K + kKBytes - 1) / kKBytes;
+    const int n_o = (N + kTileRows - 1) / kTileRows;
+    if (M <= 128) {
+        A8Plan p = {std::max(16, std::min(128, (M + 15) / 16 * 16)), 1, 0};
+        while (p.split < 8 && 2 * p.split <= nkb && n_o * 2 * p.split <= sms) p.split *= 2;
+        return p;
+    }
+    return {256, 1, 1};
+}
+
+cudaError_t launch_qgemm_a8(const A8Plan &plan, int fmt, int dtype, const void *Xq, const float *xs,
+                            const void *Wq, const float *wsc, const float *bias, void *Y, int M,
+                            int N, int K, DevCtl *ctl, cudaStream_t s) {
+    return fmt == kFmtQ8
+               ? launch_a8_y<kFmtQ8>(plan, dtype, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s)
+               : launch_a8_y<kFmtE4M3>(plan, dtype, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+}
+
+}  // namespace rtq

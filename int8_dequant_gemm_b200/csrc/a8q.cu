@@ -1,0 +1,502 @@
+// Activations into 8 bits, one scale a row: plain quantization, residual
+// addition + root-mean-square norm, and the gated SiLU, each followed in the
+// same kernel by
+//
+//   s0 = max_k |v_k| / Q,   code_k = v_k / s0 rounded to nearest even
+//
+// (Q = 127 onto int8, the rule of rt_quantize_q8_row; Q = 448 onto FP8 E4M3).
+//
+// Norm: y = h * rstd * g with rstd = 1 / sqrt(mean(h^2) + eps) > 0, so
+// y_k / max|y| = (h g)_k / max|h g|: the codes need only v = h * g, and rstd
+// enters the scale alone, scale = s0 * rstd.  Sum of squares and maximum
+// therefore come from one pass over the row and one reduction, and no value
+// waits for rstd.
+//
+// A row stays in the registers of a group of TPR threads (NV vectors of 16
+// bytes a thread and input), so each input is read once and nothing is
+// written but the sum h, the codes and the scale.  Sums, maxima and values are
+// fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace rtq {
+namespace {
+
+constexpr int kModeQuant = 0, kModeNorm = 1, kModeGate = 2;
+
+template <typename T>
+struct Vec {
+    static constexpr int n = 16 / static_cast<int>(sizeof(T));
+};
+
+__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4], const float *) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+}
+
+__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8], const __nv_bfloat16 *) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8], const __half *) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[4], const float *) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[8], const __nv_bfloat16 *) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[8], const __half *) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// |v| as bits: an order on magnitudes in which infinity is above every finite
+// value and NaN above infinity, so that one unsigned maximum finds both.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kTinyBits = 0x0D800000u;   // 2^-100: from here on 1 / (max / Q) is finite
+
+// Sum and unsigned maximum over the TPR threads of a row's group; every
+// thread gets both.  TPR > 32: through shared memory, `part` = one slot per
+// warp of the block, two buffers used in turn so that one barrier a call is
+// enough.  A group of whole warps smaller than the block syncs the block: all
+// of a block's groups run the same number of calls.
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float &sum, uint32_t &mx, float2 *part, int &turn) {
+    mx = __reduce_max_sync(0xffffffffu, mx);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        float2 *buf = part + turn * 32;
+        turn ^= 1;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) buf[warp] = make_float2(sum, __uint_as_float(mx));
+        __syncthreads();
+        const int w0 = warp / kWarps * kWarps;
+        const float2 p = buf[w0 + (lane % kWarps)];
+        mx = __reduce_max_sync(0xffffffffu, __float_as_uint(p.y));
+        sum = p.x;
+#pragma unroll
+        for (int d = kWarps / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+}
+
+// The integer nearest v / s0 (ties to even), from p within 3e-5 of the
+// quotient.  If p is near a border n + 1/2, the sign of v - (n + 1/2) s0, which
+// one fused multiply-add gives exactly, decides.  `tiny`: s0 may be subnormal,
+// where twice that difference is still a multiple of the smallest subnormal.
+__device__ __forceinline__ float nearest_code(float v, float s0, float p, bool tiny) {
+    const float lo = floorf(p);
+    const float d = tiny ? fmaf(-(2.f * lo + 1.f), s0, 2.f * v) : fmaf(-(lo + 0.5f), s0, v);
+    const float even = 2.f * floorf(0.5f * lo) == lo ? lo : lo + 1.f;
+    const float near = fabsf(p - lo - 0.5f) > 1e-4f ? rintf(p) : d > 0.f ? lo + 1.f : d < 0.f ? lo : even;
+    return fminf(127.f, fmaxf(-127.f, near));
+}
+
+// Codes of one 16-byte input vector's values.  int8: v * (1 / s0) is within
+// 3e-5 of the quotient at |code| <= 127 (two roundings of 2^-24), so only a
+// product that close to a rounding border can round to another integer than
+// the quotient; those are decided exactly, and the codes are the host
+// quantizer's.  `slow`: s0 is too small for 1 / s0.
+template <int FMT, int N>
+__device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv, bool slow,
+                                       uint32_t (&w)[N / 4]) {
+    if (FMT == kFmtQ8) {
+        float t[N], edge = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float p = v[i] * inv;
+            t[i] = rintf(p);
+            edge = fmaxf(edge, fabsf(p - t[i]));
+        }
+        if (slow || edge > 0.49997f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float p = slow ? fminf(200.f, fmaxf(-200.f, __fdiv_rn(v[i], s0))) : v[i] * inv;
+                t[i] = s0 > 0.f ? nearest_code(v[i], s0, p, slow) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            // 1.5 * 2^23 + t holds t in its low byte (two's complement)
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(t[4 * i + j] + 12582912.f);
+            w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
+                               0x5410);
+        }
+    } else {
+        float t[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            t[i] = slow ? (s0 > 0.f ? __fdiv_rn(v[i], s0) : 0.f) : v[i] * inv;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i + 2], t[4 * i + 3]),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            w[i] = lo | (hi << 16);
+        }
+    }
+}
+
+// a * sigmoid(a) * b = a b / (1 + e^-a).  e^-a overflows to infinity below
+// a = -88.7, where the quotient's true value is below 2^-120 |b|: it becomes 0.
+__device__ __forceinline__ float silu_mul(float a, float b) {
+    return __fdividef(a, 1.f + __expf(-a)) * b;
+}
+
+// One row per group of TPR threads, blockDim.x / TPR rows per block.  Inputs:
+// X [M, K] (gate: [M, 2K], the halves a | b), R [M, K] or NULL, gain [K] or
+// NULL; H [M, K] or NULL receives x + r.  H may be X or R: a thread writes
+// only vectors it has already read.
+template <typename T, int MODE, int FMT, int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+    a8_rows_kernel(const T *X, const T *R, const float *__restrict__ gain, float eps, T *H,
+                   uint8_t *__restrict__ codes, float *__restrict__ scales, int M, int K,
+                   DevCtl *ctl) {
+    constexpr int V = Vec<T>::n;
+    __shared__ float2 part[64];
+    int turn = 0;
+    // X may be the previous kernel's output, and the outputs its input.  This
+    // kernel does not release its dependents early: its codes may be the
+    // weights of the next product, whose kernels read weights before they
+    // wait for this grid.
+    pdl_wait_prior_grid();
+    const int per_block = blockDim.x / TPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / TPR;
+    const int t = threadIdx.x % TPR;
+    const bool live = row < M;            // a dead group still takes part in the barriers
+    float v[NV][V];
+    float ss = 0.f;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+        if (live && k < K) {
+            if (MODE == kModeGate) {
+                const T *p = X + row * 2 * K + k;
+                float a[V], b[V];
+                unpack(*reinterpret_cast<const uint4 *>(p), a, X);
+                unpack(*reinterpret_cast<const uint4 *>(p + K), b, X);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] = silu_mul(a[j], b[j]);
+            } else {
+                unpack(*reinterpret_cast<const uint4 *>(X + row * K + k), v[i], X);
+                if (MODE == kModeNorm && R) {
+                    float r[V];
+                    unpack(*reinterpret_cast<const uint4 *>(R + row * K + k), r, X);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[i][j] += r[j];
+                }
+            }
+        }
+    }
+    if (MODE == kModeNorm && H) {
+        // rounded once to the stream's type; the norm below is of the fp32 sum
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (live && k < K) *reinterpret_cast<uint4 *>(H + row * K + k) = pack(v[i], X);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+        if (MODE == kModeNorm) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+            if (gain && k < K) {
+#pragma unroll
+                for (int j = 0; j < V; j += 4) {
+                    const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
+                    const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx = max(mx, abs_bits(v[i][j + q] * gg[q]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) mx = max(mx, abs_bits(v[i][j]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) mx = max(mx, abs_bits(v[i][j]));
+        }
+    }
+    row_reduce<TPR>(ss, mx, part, turn);
+    float mul = 1.f;                      // scale = s0 * mul
+    if (MODE == kModeNorm) {
+        mul = __frsqrt_rn(ss / static_cast<float>(K) + eps);
+        // The squares or h * gain have left fp32's range, or the products are
+        // so small that their quotients would lose digits: the row once more
+        // as y itself, from h * 2^-80 where the squares overflowed.  A group
+        // agrees on this; groups that share barriers take the block's vote.
+        const bool redo = live && (!(ss <= FLT_MAX) || mx >= kInfBits || mx < kTinyBits);
+        const bool any = (TPR == 32 || TPR >= 256) ? redo : __syncthreads_or(redo) != 0;
+        if (any) {
+            const float f = ss <= FLT_MAX ? 1.f : 0x1p-80f;
+            float s2 = 0.f, none = 0.f;
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s2 = fmaf(v[i][j] * f, v[i][j] * f, s2);
+            row_reduce<TPR>(s2, m2, part, turn);
+            const float r2 = __frsqrt_rn(s2 / static_cast<float>(K) + eps * f * f);
+            m2 = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * TPR + t) * V;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if (redo) v[i][j] = v[i][j] * f * r2;
+                    m2 = max(m2, abs_bits(v[i][j] * (gain && k < K ? __ldg(gain + k + j) : 1.f)));
+                }
+            }
+            row_reduce<TPR>(none, m2, part, turn);
+            if (redo) {
+                mx = m2;
+                mul = 1.f;
+            }
+        }
+    }
+    if (!live) return;
+    const float amax = __uint_as_float(mx);
+    constexpr float kTop = FMT == kFmtQ8 ? 127.f : 448.f;
+    if (mx >= kInfBits) {
+        // a value that is not finite: the row has no scale; its codes are 0
+        // and the product gives NaN for it, and for it alone
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (k < K) {
+                if (V == 4)
+                    *reinterpret_cast<uint32_t *>(codes + row * K + k) = 0u;
+                else
+                    *reinterpret_cast<uint2 *>(codes + row * K + k) = make_uint2(0u, 0u);
+            }
+        }
+        if (t == 0) {
+            scales[row] = __uint_as_float(0x7FC00000u);
+            atomicOr(&ctl->status, 1u << kStatusRange);
+        }
+        return;
+    }
+    const float s0 = __fdiv_rn(amax, kTop);
+    const bool slow = mx < kTinyBits;
+    const float inv = slow ? 0.f : __fdiv_rn(1.f, s0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+        if (k >= K) continue;
+        if (MODE == kModeNorm) {
+#pragma unroll
+            for (int j = 0; j < V && gain; j += 4) {
+                const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
+                v[i][j] *= g.x;
+                v[i][j + 1] *= g.y;
+                v[i][j + 2] *= g.z;
+                v[i][j + 3] *= g.w;
+            }
+        }
+        uint32_t w[V / 4];
+        encode<FMT, V>(v[i], s0, inv, slow, w);
+        if (V == 4)
+            *reinterpret_cast<uint32_t *>(codes + row * K + k) = w[0];
+        else
+            *reinterpret_cast<uint2 *>(codes + row * K + k) = make_uint2(w[0], w[V / 4 - 1]);
+    }
+    if (t == 0) scales[row] = s0 * mul;
+}
+
+// Values of 8-bit rows: code * scale in fp32, rounded once to the type.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256)
+    a8_values_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales,
+                     T *__restrict__ out, int64_t vecs, int vk) {
+    constexpr int V = Vec<T>::n;
+    pdl_wait_prior_grid();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < vecs;
+         i += step) {
+        const float s = __ldg(scales + i / vk);
+        uint32_t w[2];
+        if (V == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(codes) + i);
+            w[1] = 0;
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(codes) + i);
+            w[0] = u.x;
+            w[1] = u.y;
+        }
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t b = (w[j >> 2] >> (8 * (j & 3))) & 0xFFu;
+            if (FMT == kFmtQ8) {
+                f[j] = static_cast<float>(static_cast<int8_t>(b)) * s;
+            } else {
+                const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b),
+                                                             __NV_E4M3);
+                f[j] = __half2float(__half(h)) * s;
+            }
+        }
+        reinterpret_cast<uint4 *>(out)[i] = pack(f, out);
+    }
+}
+
+cudaError_t launch_pdl(const void *fn, unsigned grid, unsigned block, void **args,
+                       cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+struct RowArgs {
+    const void *X, *R;
+    const float *gain;
+    float eps;
+    void *H;
+    uint8_t *codes;
+    float *scales;
+    int M, K;
+    DevCtl *ctl;
+};
+
+template <typename T, int MODE, int FMT, int TPR, int NV>
+cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
+    constexpr int kBlock = TPR < 256 ? 256 : TPR;
+    constexpr int kRows = kBlock / TPR;
+    const T *X = static_cast<const T *>(a.X), *R = static_cast<const T *>(a.R);
+    T *H = static_cast<T *>(a.H);
+    void *args[] = {&X, &R, &a.gain, &a.eps, &H, &a.codes, &a.scales, &a.M, &a.K, &a.ctl};
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
+    // few rows: no more threads than they need
+    const unsigned block = a.M < kRows ? static_cast<unsigned>(a.M * TPR) : kBlock;
+    return launch_pdl(reinterpret_cast<const void *>(a8_rows_kernel<T, MODE, FMT, TPR, NV>), grid,
+                      block, args, s);
+}
+
+// Threads a row: the fewest whose vectors fit in 16 values (fp32) or 32
+// values (16-bit types) a thread.
+template <typename T, int MODE, int FMT>
+cudaError_t launch_rows_k(const RowArgs &a, cudaStream_t s) {
+    const int vecs = a.K / Vec<T>::n;
+    constexpr int NV = 4;
+    if (vecs <= 32) return launch_rows<T, MODE, FMT, 32, 1>(a, s);
+    if (vecs <= 64) return launch_rows<T, MODE, FMT, 32, 2>(a, s);
+    if (vecs <= 32 * NV) return launch_rows<T, MODE, FMT, 32, NV>(a, s);
+    if (vecs <= 64 * NV) return launch_rows<T, MODE, FMT, 64, NV>(a, s);
+    if (vecs <= 128 * NV) return launch_rows<T, MODE, FMT, 128, NV>(a, s);
+    if (vecs <= 256 * NV) return launch_rows<T, MODE, FMT, 256, NV>(a, s);
+    if (vecs <= 512 * NV) return launch_rows<T, MODE, FMT, 512, NV>(a, s);
+    if (Vec<T>::n == 8 || vecs <= 1024 * NV) return launch_rows<T, MODE, FMT, 1024, NV>(a, s);
+    return launch_rows<T, MODE, FMT, 1024, Vec<T>::n == 4 ? 8 : NV>(a, s);   // up to kMaxRowK
+}
+
+template <typename T, int MODE>
+cudaError_t launch_rows_f(int fmt, const RowArgs &a, cudaStream_t s) {
+    return fmt == kFmtQ8 ? launch_rows_k<T, MODE, kFmtQ8>(a, s)
+                         : launch_rows_k<T, MODE, kFmtE4M3>(a, s);
+}
+
+template <int MODE>
+cudaError_t launch_rows_t(int fmt, int dtype, const RowArgs &a, cudaStream_t s) {
+    if (dtype == RT_DTYPE_F32) return launch_rows_f<float, MODE>(fmt, a, s);
+    if (dtype == RT_DTYPE_F16) return launch_rows_f<__half, MODE>(fmt, a, s);
+    return launch_rows_f<__nv_bfloat16, MODE>(fmt, a, s);
+}
+
+template <typename T>
+cudaError_t launch_values(int fmt, const uint8_t *codes, const float *scales, T *out, int M, int K,
+                          cudaStream_t s) {
+    int64_t vecs = static_cast<int64_t>(M) * (K / Vec<T>::n);
+    int vk = K / Vec<T>::n;
+    void *args[] = {&codes, &scales, &out, &vecs, &vk};
+    const int64_t want = (vecs + 255) / 256;
+    const unsigned grid = static_cast<unsigned>(want < 148 * 16 ? want : 148 * 16);
+    const void *fn = fmt == kFmtQ8 ? reinterpret_cast<const void *>(a8_values_kernel<T, kFmtQ8>)
+                                   : reinterpret_cast<const void *>(a8_values_kernel<T, kFmtE4M3>);
+    return launch_pdl(fn, grid, 256, args, s);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_a8(int fmt, int dtype, const void *X, uint8_t *codes, float *scales,
+                               int M, int K, DevCtl *ctl, cudaStream_t s) {
+    return launch_rows_t<kModeQuant>(
+        fmt, dtype, {X, nullptr, nullptr, 0.f, nullptr, codes, scales, M, K, ctl}, s);
+}
+
+cudaError_t launch_addnorm_a8(int fmt, int dtype, const void *X, const void *R, const float *gain,
+                              float eps, void *H, uint8_t *codes, float *scales, int M, int K,
+                              DevCtl *ctl, cudaStream_t s) {
+    return launch_rows_t<kModeNorm>(fmt, dtype, {X, R, gain, eps, H, codes, scales, M, K, ctl}, s);
+}
+
+cudaError_t launch_gate_a8(int fmt, int dtype, const void *U, uint8_t *codes, float *scales, int M,
+                           int F, DevCtl *ctl, cudaStream_t s) {
+    return launch_rows_t<kModeGate>(
+        fmt, dtype, {U, nullptr, nullptr, 0.f, nullptr, codes, scales, M, F, ctl}, s);
+}
+
+cudaError_t launch_dequant_a8(int fmt, int dtype, const uint8_t *codes, const float *scales,
+                              void *out, int M, int K, cudaStream_t s) {
+    if (dtype == RT_DTYPE_F32)
+        return launch_values(fmt, codes, scales, static_cast<float *>(out), M, K, s);
+    if (dtype == RT_DTYPE_F16)
+        return launch_values(fmt, codes, scales, static_cast<__half *>(out), M, K, s);
+    return launch_values(fmt, codes, scales, static_cast<__nv_bfloat16 *>(out), M, K, s);
+}
+
+}  // namespace rtq

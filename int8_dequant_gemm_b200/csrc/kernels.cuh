@@ -197,6 +197,33 @@ size_t pl_workspace_bytes(const PlInput *in, int count, int M);
 cudaError_t launch_pl_batch(const PlInput *in, int count, int M, void *ws, DevCtl *ctl,
                             cudaStream_t s);
 
+// Activations into 8 bits with one scale a row (a8q.cu), and the product of
+// 8-bit activations with 8-bit weights (a8.cu).  Arguments are validated by
+// the caller (a8api.cu).  Rows of the row kernels stay in registers, which
+// bounds their length.
+constexpr int kMaxRowK = 32768;
+cudaError_t launch_quantize_a8(int fmt, int dtype, const void *X, uint8_t *codes, float *scales,
+                               int M, int K, DevCtl *ctl, cudaStream_t s);
+cudaError_t launch_addnorm_a8(int fmt, int dtype, const void *X, const void *R, const float *gain,
+                              float eps, void *H, uint8_t *codes, float *scales, int M, int K,
+                              DevCtl *ctl, cudaStream_t s);
+cudaError_t launch_gate_a8(int fmt, int dtype, const void *U, uint8_t *codes, float *scales, int M,
+                           int F, DevCtl *ctl, cudaStream_t s);
+cudaError_t launch_dequant_a8(int fmt, int dtype, const uint8_t *codes, const float *scales,
+                              void *out, int M, int K, cudaStream_t s);
+
+// The tile plan of an 8-bit product: activation rows per tile, K slices
+// (CTAs of a cluster that share a tile's K), and whether CTA pairs share one
+// MMA.  plan_a8 picks it from the shape and the SM count.
+struct A8Plan {
+    int bn, split, pair;
+};
+int sm_count();                        // of the current device (cached)
+A8Plan plan_a8(int M, int N, int K, int sms);
+cudaError_t launch_qgemm_a8(const A8Plan &plan, int fmt, int dtype, const void *Xq, const float *xs,
+                            const void *Wq, const float *wsc, const float *bias, void *Y, int M,
+                            int N, int K, DevCtl *ctl, cudaStream_t s);
+
 // dequantization exports (same __device__ routines as the GEMMs)
 cudaError_t launch_dequant_q4_f32(const uint8_t *Wq, const uint16_t *SM, float *W, int N, int K,
                                   cudaStream_t s);
