@@ -114,9 +114,57 @@ __device__ __forceinline__ __half to_type(float v, const __half *) { return __fl
 __device__ __forceinline__ __nv_bfloat16 to_type(float v, const __nv_bfloat16 *) {
     return __float2bfloat16_rn(v);
 }
+__device__ __forceinline__ uint32_t bits16(float) { return 0; }
+__device__ __forceinline__ uint32_t bits16(__half v) { return __half_as_ushort(v); }
+__device__ __forceinline__ uint32_t bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// One epilogue warp's 16 columns (activation rows) of its 32 outputs a row:
+// scale, round, store.  All of a chunk's scales are read before its first
+// store, which they could alias for the compiler.  `whole`: every lane has an
+// output.  16-bit results of even rows go out as pairs: lanes 2i and 2i + 1
+// trade one value of two rows, and each stores two neighbours of one row.
+template <int FMT, typename YT>
+__device__ __forceinline__ void store_chunk(const uint32_t (&v)[16], const float *xs, float wsc,
+                                            float bo, YT *yo, int N, int rows, bool live, bool whole,
+                                            float &nf) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(xs)[i];
+        x[4 * i] = f.x;
+        x[4 * i + 1] = f.y;
+        x[4 * i + 2] = f.z;
+        x[4 * i + 3] = f.w;
+    }
+    YT y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        y[i] = to_type(fmaf(acc_f32<FMT>(v[i]) * wsc, x[i], bo), yo);
+        nf = fmaf(to_f32(y[i]), 0.f, nf);
+    }
+    const size_t ld = static_cast<size_t>(N);
+    if (sizeof(YT) == 2 && whole && rows >= 16 && (N & 1) == 0) {
+        const int odd = threadIdx.x & 1;
+        yo -= odd;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const uint32_t a = bits16(y[i]), b = bits16(y[i + 1]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            const uint32_t w = odd ? got | (b << 16) : a | (got << 16);
+            *reinterpret_cast<uint32_t *>(yo + static_cast<size_t>(i + odd) * ld) = w;
+        }
+    } else if (whole && rows >= 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) yo[static_cast<size_t>(i) * ld] = y[i];
+    } else if (live) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < rows) yo[static_cast<size_t>(i) * ld] = y[i];
+    }
+}
 
 // Tile t of the walk: bands of kBand activation tiles, all weight tiles of a
 // band, activation tile fastest.  The tiles that run at once then share few
@@ -337,18 +385,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const uint32_t tb = tq + static_cast<uint32_t>(b * a.bn);
             YT *yo = Y + static_cast<size_t>(m0) * a.N + o;
-            for (int c = 16 * h; c < a.bn; c += 32) {
-                uint32_t v[16];
-                tmem_ld_x16(tb + static_cast<uint32_t>(c), v);
-                tmem_ld_wait();
-                const int n = live ? min(16, mlim - c) : 0;
+            const bool whole = __all_sync(0xffffffffu, live);
+            uint32_t v[2][16];
+            if (16 * h < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(16 * h), v[0]);
+            for (int c = 16 * h, u = 0; c < a.bn; c += 64) {
+                // two chunks a turn, the next one's TMEM load under this one's stores
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (i < n) {
-                        const YT y = to_type(fmaf(acc_f32<FMT>(v[i]) * wsc, xs_t[c + i], bo), Y);
-                        nf = fmaf(to_f32(y), 0.f, nf);
-                        yo[static_cast<size_t>(c + i) * a.N] = y;
-                    }
+                for (u = 0; u < 2; ++u) {
+                    const int cc = c + 32 * u;
+                    if (cc >= a.bn) break;
+                    tmem_ld_wait();
+                    if (cc + 32 < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(cc + 32), v[u ^ 1]);
+                    store_chunk<FMT>(v[u], xs_t + cc, wsc, bo, yo + static_cast<size_t>(cc) * a.N,
+                                     a.N, mlim - cc, live, whole, nf);
                 }
             }
             tc_fence_before_sync();
