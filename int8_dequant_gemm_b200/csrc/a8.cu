@@ -11,11 +11,15 @@
 //
 // Orientation as in the other tensor-core kernels: weight rows are the MMA's M
 // (TMEM lanes), activation rows its N (TMEM columns).  A warp of the epilogue
-// then holds 32 consecutive outputs of one Y row, so plain stores are whole
-// 128-byte segments of Y for every N and alignment.
+// then holds 32 neighbouring outputs of one Y row, so plain stores are whole
+// 128-byte segments of Y for every N, and few activation rows cost few columns.
+// Measured and not kept: activation rows in lanes with 32-byte stores (a quarter
+// of the store instructions; 276 against 204 us for 65536 x 4096 x 512 into
+// fp32, 181 against 175 into bf16), and tiles of Y staged in shared memory and
+// stored by TMA (19.8 against 17.5 us for 4096 x 4096 x 512).
 //
-// Roles (12 warps): warp 0 TMA, warp 1 MMA issue, warps 4-11 epilogue (two per
-// TMEM lane quadrant, alternating 16-column chunks); warps 2-3 idle.
+// Roles (20 warps): warp 0 TMA, warp 1 MMA issue, warps 4-19 epilogue (four per
+// TMEM lane quadrant); warps 2-3 idle.
 //
 // Three shapes of the same code:
 //   - persistent tiles of 128 weight rows x bn activation rows, one CTA each,
@@ -39,31 +43,38 @@ namespace {
 
 constexpr int kKBytes = 128;                       // K per stage: one swizzled row
 constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights a stage
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
-constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;   // 384
+constexpr int kEpiGroups = 4;                      // of four warps, one per TMEM lane quadrant
+constexpr int kEpiWarp0 = 4, kEpiWarps = 4 * kEpiGroups, kEpiThreads = kEpiWarps * 32;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;   // 640
 constexpr int kMaxBn = 256, kMaxStages = 8;
 constexpr int kBand = 8;                           // activation tiles walked together
-constexpr uint32_t kEpiBar = 1;                    // named barrier of the epilogue warps
+constexpr uint32_t kEpiBar = 1;                    // named barriers: an epilogue set (1, 2)
 constexpr uint16_t kBoth = 3;                      // multicast mask: both CTAs of a pair
 constexpr int kSmemMax = 200 * 1024;               // ring of stages
+constexpr int kChunk = 16;                         // activation rows an epilogue warp takes at once
 
 struct A8Args {
     const float *xs, *ws, *bias;
     void *Y;
-    int M, N, K, bn, stages, split, n_o, n_m, acc_cols;
+    int M, N, K, bn, stages, split;
+    int n_o, n_m;            // weight tiles, activation tiles
+    int acc_cols;
+    int alt;                 // two epilogue sets take turns
+    int tail_off;            // after the ring: activation scales [4][kMaxBn],
+                             // barriers and words
 };
 
 __host__ __device__ constexpr int stage_bytes(int bn, int pair) {
     return kABytes + (pair ? bn / 2 : bn) * kKBytes;
 }
 
-// Ring, then xs[2][kMaxBn], then the barriers and words below.
-__host__ __device__ inline int tail_offset(const A8Args &a, int pair) {
+// The ring; a split's partial sums reuse it.
+__host__ inline int ring_bytes(const A8Args &a, int pair) {
     const int ring = a.stages * stage_bytes(a.bn, pair);
-    const int red = a.split > 1 ? a.bn * kTileRows * 4 : 0;   // partial sums reuse the ring
+    const int red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
     return ring > red ? ring : red;
 }
-constexpr int kTailBytes = 2 * kMaxBn * 4 + (2 * kMaxStages + 5) * 8 + 16;
+constexpr int kTailBytes = 4 * kMaxBn * 4 + (2 * kMaxStages + 5) * 8 + 16;
 
 // Instruction descriptors (A and B K-major): accumulator s32 (2) or f32 (1),
 // operand type 1 = s8 of kind::i8, 0 = e4m3 of kind::f8f6f4.
@@ -114,55 +125,107 @@ __device__ __forceinline__ __half to_type(float v, const __half *) { return __fl
 __device__ __forceinline__ __nv_bfloat16 to_type(float v, const __nv_bfloat16 *) {
     return __float2bfloat16_rn(v);
 }
-__device__ __forceinline__ uint32_t bits16(float) { return 0; }
-__device__ __forceinline__ uint32_t bits16(__half v) { return __half_as_ushort(v); }
-__device__ __forceinline__ uint32_t bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// One epilogue warp's 16 columns (activation rows) of its 32 outputs a row:
-// scale, round, store.  All of a chunk's scales are read before its first
-// store, which they could alias for the compiler.  `whole`: every lane has an
-// output.  16-bit results of even rows go out as pairs: lanes 2i and 2i + 1
-// trade one value of two rows, and each stores two neighbours of one row.
+// Two results of one output column (rows i, i + 1) as one register of the type.
+__device__ __forceinline__ uint32_t pair_bits(float a, float b, const __half *) {
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t pair_bits(float a, float b, const __nv_bfloat16 *) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Turns NaN in either half once a result is not finite in its type.
+__device__ __forceinline__ void watch(uint32_t &nf, uint32_t w, const __half *) {
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(nf) : "r"(w), "r"(0u));
+}
+__device__ __forceinline__ void watch(uint32_t &nf, uint32_t w, const __nv_bfloat16 *) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(nf) : "r"(w), "r"(0u));
+}
+__device__ __forceinline__ void watch(uint32_t &nf, float v) {
+    nf = __float_as_uint(fmaf(v, 0.f, __uint_as_float(nf)));
+}
+
+// A chunk of 16 activation rows of one weight row: y = acc * ws * xs + bias in
+// fp32 (fp32 results), or rounded and packed, rows 2i and 2i + 1 in word i
+// (16-bit results).  `xs`: the rows' scales in shared memory.
 template <int FMT, typename YT>
-__device__ __forceinline__ void store_chunk(const uint32_t (&v)[16], const float *xs, float wsc,
-                                            float bo, YT *yo, int N, int rows, bool live, bool whole,
-                                            float &nf) {
-    float x[16];
+__device__ __forceinline__ void finish_chunk(uint32_t (&v)[kChunk], uint32_t xs, float ws, float bo,
+                                             uint32_t &nf, const YT *type) {
+    const float2 ws2 = make_float2(ws, ws), bo2 = make_float2(bo, bo);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 f = reinterpret_cast<const float4 *>(xs)[i];
-        x[4 * i] = f.x;
-        x[4 * i + 1] = f.y;
-        x[4 * i + 2] = f.z;
-        x[4 * i + 3] = f.w;
-    }
-    YT y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        y[i] = to_type(fmaf(acc_f32<FMT>(v[i]) * wsc, x[i], bo), yo);
-        nf = fmaf(to_f32(y[i]), 0.f, nf);
-    }
-    const size_t ld = static_cast<size_t>(N);
-    if (sizeof(YT) == 2 && whole && rows >= 16 && (N & 1) == 0) {
-        const int odd = threadIdx.x & 1;
-        yo -= odd;
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const uint32_t a = bits16(y[i]), b = bits16(y[i + 1]);
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-            const uint32_t w = odd ? got | (b << 16) : a | (got << 16);
-            *reinterpret_cast<uint32_t *>(yo + static_cast<size_t>(i + odd) * ld) = w;
+    for (int i = 0; i < kChunk; i += 4) {
+        const uint4 f = lds_v4(xs + 4 * i);
+        const float2 x0 = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+        const float2 x1 = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+        const float2 a0 = make_float2(acc_f32<FMT>(v[i]), acc_f32<FMT>(v[i + 1]));
+        const float2 a1 = make_float2(acc_f32<FMT>(v[i + 2]), acc_f32<FMT>(v[i + 3]));
+        const float2 y0 = __ffma2_rn(__fmul2_rn(a0, ws2), x0, bo2);
+        const float2 y1 = __ffma2_rn(__fmul2_rn(a1, ws2), x1, bo2);
+        if constexpr (sizeof(YT) == 2) {
+            v[i / 2] = pair_bits(y0.x, y0.y, type);
+            v[i / 2 + 1] = pair_bits(y1.x, y1.y, type);
+            watch(nf, v[i / 2], type);
+            watch(nf, v[i / 2 + 1], type);
+        } else {
+            watch(nf, y0.x);
+            watch(nf, y0.y);
+            watch(nf, y1.x);
+            watch(nf, y1.y);
+            v[i] = __float_as_uint(y0.x);
+            v[i + 1] = __float_as_uint(y0.y);
+            v[i + 2] = __float_as_uint(y1.x);
+            v[i + 3] = __float_as_uint(y1.y);
         }
-    } else if (whole && rows >= 16) {
+    }
+}
+
+// A finished chunk of one weight row: yo = this lane's output of its first row.
+// `whole`: every lane of the warp has an output.  16-bit results of an even N
+// go out as pairs: lanes 2i and 2i + 1 trade one value of two rows, and each
+// stores two neighbours of one row.
+template <typename YT>
+__device__ __forceinline__ void store_chunk(const uint32_t (&v)[kChunk], YT *yo, int N, int rows,
+                                            bool live, bool whole) {
+    const size_t ld = static_cast<size_t>(N);
+    if constexpr (sizeof(YT) == 2) {
+        if (whole && rows >= kChunk && (N & 1) == 0) {
+            const int odd = threadIdx.x & 1;
+            const uint32_t sel = odd ? 0x3276u : 0x5410u;
+            YT *yp = yo + static_cast<size_t>(odd) * ld - odd;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) yo[static_cast<size_t>(i) * ld] = y[i];
-    } else if (live) {
+            for (int i = 0; i < kChunk / 2; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, v[i], 1);
+                *reinterpret_cast<uint32_t *>(yp + static_cast<size_t>(2 * i) * ld) =
+                    __byte_perm(v[i], got, sel);
+            }
+            return;
+        }
+        uint16_t *yh = reinterpret_cast<uint16_t *>(yo);
+        if (whole && rows >= kChunk) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < rows) yo[static_cast<size_t>(i) * ld] = y[i];
+            for (int i = 0; i < kChunk; ++i)
+                yh[static_cast<size_t>(i) * ld] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (i < rows)
+                    yh[static_cast<size_t>(i) * ld] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+        }
+    } else {
+        float *yf = reinterpret_cast<float *>(yo);
+        if (whole && rows >= kChunk) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) yf[static_cast<size_t>(i) * ld] = __uint_as_float(v[i]);
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (i < rows) yf[static_cast<size_t>(i) * ld] = __uint_as_float(v[i]);
+        }
     }
 }
 
@@ -182,15 +245,15 @@ struct TileAt {
 
 template <int FMT, typename YT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    a8_qgemm_kernel(const __grid_constant__ CUtensorMap x_map,
-                    const __grid_constant__ CUtensorMap w_map, const A8Args a, DevCtl *ctl) {
+    a8_qgemm_kernel(const __grid_constant__ CUtensorMap w_map,
+                    const __grid_constant__ CUtensorMap x_map, const A8Args a, DevCtl *ctl) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_addr(smem);
-    uint8_t *tail = smem + tail_offset(a, PAIR);
+    uint8_t *tail = smem + a.tail_off;
     float *xs_s = reinterpret_cast<float *>(tail);
-    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 2 * kMaxBn * 4);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 4 * kMaxBn * 4);
     uint64_t *empty = full + kMaxStages;
     uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -216,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * kEpiWarps);
+            mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * kEpiWarps / 2);
         }
         mbar_init(drain, 1);
         *failed = 0;
@@ -249,7 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int s = 0, j = 0;
             uint32_t par = 1;
-            const uint32_t xb = static_cast<uint32_t>(sbytes - kABytes);
             for (int t = first; t < n_tiles && ok; t += step) {
                 const TileAt at(t, a.n_m, a.n_o);
                 const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
@@ -267,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!skip) tma_load_2d_pair(dst, &w_map, kb * kKBytes, oy, cbar);
                         tma_load_2d_pair(dst + kABytes, &x_map, kb * kKBytes, my, cbar);
                     } else {
-                        mbar_expect_tx(&full[s], kABytes + xb);
+                        mbar_expect_tx(&full[s], static_cast<uint32_t>(sbytes));
                         if (!skip) tma_load_2d(dst, &w_map, kb * kKBytes, oy, &full[s]);
                         tma_load_2d(dst + kABytes, &x_map, kb * kKBytes, my, &full[s]);
                     }
@@ -344,13 +406,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kEpiWarp0) {
         // ============================================================ epilogue
-        const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
-        const int et = static_cast<int>(threadIdx.x) - kEpiWarp0 * 32;
+        // Several tiles a CTA (alt): two sets of eight warps take turns, so that
+        // one set's loads and arithmetic run under the other's stores and each
+        // has two tiles' time for its latencies.  One tile: all 16 warps share it.
+        const int q = warp & 3;
+        const int ew = warp - kEpiWarp0;
+        const int set = a.alt ? ew >> 3 : 0, groups = a.alt ? kEpiGroups / 2 : kEpiGroups;
+        const int h = a.alt ? (ew >> 2) & 1 : ew >> 2;
+        const int et = (static_cast<int>(threadIdx.x) - kEpiWarp0 * 32) & (groups * 128 - 1);
+        const int turn = a.alt ? 2 : 1, chunk_step = 2 * kChunk * groups;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
         YT *const Y = static_cast<YT *>(a.Y);
-        float nf = 0.f;                      // NaN once an output is not finite
-        int n_local = 0;
-        for (int t = first; t < n_tiles && ok; t += step, ++n_local) {
+        uint32_t nf = 0;                     // NaN once an output is not finite
+        // the next tile's scales and bias are loaded while this one is stored:
+        // activation row et's scale by thread et, this lane's by every warp
+        float x_next = 0.f, w_next = 1.f, b_next = 0.f;
+        auto fetch = [&](int t) {
+            if (split > 1 || t >= n_tiles) return;
+            const TileAt at(t, a.n_m, a.n_o);
+            const int m = at.m * a.bn + et;
+            if (et < a.bn && m < a.M) x_next = __ldg(a.xs + m);
+            const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
+            if (o < a.N) {
+                if (a.ws) w_next = __ldg(a.ws + o);
+                if (a.bias) b_next = __ldg(a.bias + o);
+            }
+        };
+        fetch(first + set * step);
+        int n_local = set;
+        for (int t = first + set * step; t < n_tiles && ok; t += turn * step, n_local += turn) {
             const TileAt at(t, a.n_m, a.n_o);
             const int b = n_local & 1;
             const int m0 = at.m * a.bn;
@@ -361,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t *red = reinterpret_cast<uint32_t *>(smem);
-                for (int c = 16 * h; c < a.bn; c += 32) {
+                for (int c = kChunk * h; c < a.bn; c += kChunk * kEpiGroups) {
                     uint32_t v[16];
                     tmem_ld_x16(tq + static_cast<uint32_t>(c), v);
                     tmem_ld_wait();
@@ -372,13 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 continue;
             }
-            float *xs_t = xs_s + b * kMaxBn;
-            xs_t[et] = et < mlim ? __ldg(a.xs + m0 + et) : 0.f;
+            float *xs_t = xs_s + (2 * b + ((n_local >> 1) & 1)) * kMaxBn;
+            if (et < kMaxBn) xs_t[et] = x_next;
+            const float ws = w_next, bo = b_next;
             const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
             const bool live = o < a.N;
-            const float wsc = live && a.ws ? __ldg(a.ws + o) : 1.f;
-            const float bo = live && a.bias ? __ldg(a.bias + o) : 0.f;
-            named_bar_sync(kEpiBar, kEpiThreads);
+            fetch(t + turn * step);
+            named_bar_sync(kEpiBar + set, groups * 128);
             ok = __all_sync(0xffffffffu,
                             mbar_wait(&acc_full[b], static_cast<uint32_t>(n_local / 2) & 1u, lim));
             if (!ok) break;
@@ -386,28 +470,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tb = tq + static_cast<uint32_t>(b * a.bn);
             YT *yo = Y + static_cast<size_t>(m0) * a.N + o;
             const bool whole = __all_sync(0xffffffffu, live);
-            uint32_t v[2][16];
-            if (16 * h < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(16 * h), v[0]);
-            for (int c = 16 * h, u = 0; c < a.bn; c += 64) {
-                // two chunks a turn, the next one's TMEM load under this one's stores
-#pragma unroll
-                for (u = 0; u < 2; ++u) {
-                    const int cc = c + 32 * u;
-                    if (cc >= a.bn) break;
-                    tmem_ld_wait();
-                    if (cc + 32 < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(cc + 32), v[u ^ 1]);
-                    store_chunk<FMT>(v[u], xs_t + cc, wsc, bo, yo + static_cast<size_t>(cc) * a.N,
-                                     a.N, mlim - cc, live, whole, nf);
+            const auto put = [&](uint32_t (&v)[kChunk], int c) {
+                finish_chunk<FMT>(v, smem_addr(xs_t + c), ws, bo, nf, Y);
+                store_chunk(v, yo + static_cast<size_t>(c) * a.N, a.N, mlim - c, live, whole);
+            };
+            int c = 2 * kChunk * h;
+            do {
+                uint32_t v0[kChunk], v1[kChunk];
+                if (c < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(c), v0);
+                if (c + kChunk < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(c + kChunk), v1);
+                tmem_ld_wait();
+                if (c + chunk_step >= a.bn) {    // the accumulator has been read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_remote(cluster_map(smem_addr(&acc_empty[b]), 0));
+                        else mbar_arrive(&acc_empty[b]);
+                    }
                 }
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_remote(cluster_map(smem_addr(&acc_empty[b]), 0));
-                else mbar_arrive(&acc_empty[b]);
-            }
+                if (c < a.bn) put(v0, c);
+                if (c + kChunk < a.bn) put(v1, c + kChunk);
+                c += chunk_step;
+            } while (c < a.bn);
         }
-        if (__any_sync(0xffffffffu, nf != 0.f) && lane == 0)
+        if (__any_sync(0xffffffffu, (nf & 0x7FFF7FFFu) != 0) && lane == 0)
             atomicOr(&ctl->status, 1u << kStatusRange);
     }
     if (!ok) {
@@ -505,8 +591,8 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     a.split = PAIR ? 1 : plan.split;
     const int nkb = (K + kKBytes - 1) / kKBytes;
     const int ot = PAIR ? 2 * kTileRows : kTileRows;
-    a.n_o = (N + ot - 1) / ot;
-    a.n_m = (M + a.bn - 1) / a.bn;
+    a.n_o = static_cast<int>((static_cast<int64_t>(N) + ot - 1) / ot);
+    a.n_m = static_cast<int>((static_cast<int64_t>(M) + a.bn - 1) / a.bn);
     a.stages = std::min(kMaxStages, kSmemMax / stage_bytes(a.bn, PAIR));
     const int64_t tiles = static_cast<int64_t>(a.n_o) * a.n_m;
     if (tiles > (int64_t(1) << 30)) return cudaErrorInvalidValue;
@@ -515,6 +601,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     while (acc < (a.split > 1 ? 1 : 2) * a.bn) acc *= 2;
     a.acc_cols = acc;
 
+    a.tail_off = ring_bytes(a, PAIR);
     CUtensorMap x_map, w_map;
     if (!encode_tma_2d(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Xq, K, M, kKBytes,
                        CU_TENSOR_MAP_SWIZZLE_128B, PAIR ? a.bn / 2 : a.bn) ||
@@ -523,7 +610,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = tail_offset(a, PAIR) + kTailBytes + 1024;
+    cfg.dynamicSmemBytes = a.tail_off + kTailBytes + 1024;
     cfg.stream = st;
     int grid;
     if (PAIR) {
@@ -536,6 +623,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
         grid = a.split > 1 ? static_cast<int>(tiles) * a.split
                            : static_cast<int>(std::min<int64_t>(tiles, sm_count()));
     }
+    a.alt = a.split == 1 && tiles > grid / (PAIR ? 2 : 1);
     cfg.gridDim = dim3(grid, 1, 1);
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -550,7 +638,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, a8_qgemm_kernel<FMT, YT, PAIR>, x_map, w_map, a, ctl);
+    return cudaLaunchKernelEx(&cfg, a8_qgemm_kernel<FMT, YT, PAIR>, w_map, x_map, a, ctl);
 }
 
 template <int FMT, typename YT>
