@@ -581,9 +581,10 @@ rt_status rt_qgemm_a8(int fmt, int dtype, const void *Xq, const float *x_scales,
                       int64_t K, void *stream);
 
 /* How rt_qgemm_a8 tiles this product on the current device: *tile_rows
- * activation rows and *split CTAs to a tile; returns 1 where CTA pairs share an
- * MMA over 256 weight rows, 0 for 128 weight rows to a CTA, -1 for sizes the
- * product refuses.  Without a device, the plan for 148 SMs. */
+ * activation rows and *split CTAs to a tile.  Returns -1 for sizes the product
+ * refuses, else the sum of 1 where CTA pairs share an MMA over 256 weight rows
+ * (otherwise 128 to a CTA) and 2 where a CTA takes one tile or one slice of its
+ * K (otherwise CTAs walk the tiles).  Without a device, the plan for 148 SMs. */
 int rt_qgemm_a8_plan(int64_t M, int64_t N, int64_t K, int *tile_rows, int *split);
 
 /*

@@ -660,11 +660,13 @@ def qgemm_a8(fmt, Xq, x_scales, Wq, w_scales=None, bias=None, Y=None, dtype=None
 
 def a8_plan(M, N, K):
     """How qgemm_a8 tiles these sizes on the current device: a dict of `rows`
-    (activation rows a tile), `split` (CTAs that share a tile's K) and `pair`
-    (CTA pairs share an MMA); None for sizes it refuses."""
+    (activation rows a tile), `split` (CTAs that share a tile's K), `pair`
+    (CTA pairs share an MMA) and `walk` (CTAs walk several tiles); None for
+    sizes it refuses."""
     rows, split = _i32(), _i32()
     r = rt_qgemm_a8_plan(M, N, K, ctypes.byref(rows), ctypes.byref(split))
-    return None if r < 0 else {"rows": rows.value, "split": split.value, "pair": bool(r)}
+    return None if r < 0 else {"rows": rows.value, "split": split.value, "pair": bool(r & 1),
+                               "walk": not r & 2}
 
 
 @dataclass

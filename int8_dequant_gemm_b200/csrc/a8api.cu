@@ -160,7 +160,7 @@ int rt_qgemm_a8_plan(int64_t M, int64_t N, int64_t K, int *tile_rows, int *split
                                        static_cast<int>(K), rtq::sm_count());
     if (tile_rows) *tile_rows = p.bn;
     if (split) *split = p.split;
-    return p.pair;
+    return p.pair | (p.small << 1);
 }
 
 }  // extern "C"

@@ -213,10 +213,11 @@ cudaError_t launch_dequant_a8(int fmt, int dtype, const uint8_t *codes, const fl
                               void *out, int M, int K, cudaStream_t s);
 
 // The tile plan of an 8-bit product: activation rows per tile, K slices
-// (CTAs of a cluster that share a tile's K), and whether CTA pairs share one
-// MMA.  plan_a8 picks it from the shape and the SM count.
+// (CTAs of a cluster that share a tile's K), whether CTA pairs share one MMA,
+// and whether CTAs of 192 threads take one tile each (bn <= 128; always so
+// with a split).  plan_a8 picks it from the shape and the SM count.
 struct A8Plan {
-    int bn, split, pair;
+    int bn, split, pair, small;
 };
 int sm_count();                        // of the current device (cached)
 A8Plan plan_a8(int M, int N, int K, int sms);

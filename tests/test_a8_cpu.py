@@ -104,9 +104,10 @@ def test_product_plan():
                 nkb = -(-K // 128)
                 assert 1 <= p["split"] <= min(8, nkb)
                 assert p["rows"] % (32 if p["pair"] else 16) == 0 and 16 <= p["rows"] <= 256
-                assert not (p["pair"] and p["split"] > 1)
+                assert not (p["pair"] and p["split"] > 1) and not (p["walk"] and p["split"] > 1)
+                assert p["walk"] or (p["rows"] <= 128 and not p["pair"])
                 if p["split"] > 1:                # partial sums fit where the ring was
-                    assert p["rows"] * 512 <= 200 * 1024
+                    assert p["rows"] * 512 <= 100 * 1024
 
 
 def test_helpers_refuse_host_tensors_and_formats():

@@ -280,7 +280,8 @@ SIZES = [(1, 1, 16), (1, 4096, 512), (2, 7, 32), (15, 130, 144), (16, 128, 128),
          (77, 200, 144), (80, 512, 2048), (80, 512, 512), (80, 2048, 512), (127, 1000, 400),
          (128, 129, 4112), (129, 300, 272), (130, 1, 16), (200, 2048, 512), (256, 256, 1024),
          (257, 513, 640), (300, 512, 2048), (513, 384, 128), (1000, 1003, 1040), (1024, 4096, 512),
-         (2049, 512, 2064), (4096, 512, 512)]
+         (2049, 512, 2064), (4096, 512, 512), (2500, 1000, 512), (3001, 2000, 400),
+         (5003, 1003, 1040), (4100, 2200, 2048), (9000, 515, 256), (7, 5000, 2048), (520, 4999, 1024)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -301,8 +302,9 @@ def test_product(rtq, M, N, K, fmt):
 
 def test_product_sizes_take_every_plan(rtq):
     plans = [rtq.a8_plan(*n) for n in SIZES]
-    assert any(p["pair"] for p in plans) and any(p["split"] > 1 for p in plans)
-    assert any(not p["pair"] and p["split"] == 1 for p in plans)
+    assert {p["split"] for p in plans} >= {1, 2, 4, 8}
+    assert any(not p["walk"] and p["split"] == 1 for p in plans)
+    assert any(p["walk"] and p["pair"] for p in plans) and any(p["walk"] and not p["pair"] for p in plans)
 
 
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
@@ -477,7 +479,7 @@ def test_explicit_stream_and_one_buffer_reused(rtq):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M,N,K", [(80, 512, 2048), (100, 30000, 128), (1500, 512, 512)])
+@pytest.mark.parametrize("M,N,K", [(80, 512, 2048), (100, 30000, 128), (2500, 1000, 512), (5003, 1003, 1040)])
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
 def test_injected_missing_box_times_out_and_recovers(rtq, M, N, K, fmt):
     xc, xs, wc, ws, b = operands(fmt, M, N, K, seed=13)
