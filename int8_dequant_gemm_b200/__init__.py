@@ -460,15 +460,15 @@ def qgemm_noalloc(fmt, X, Wq, scales, Y, path="auto", stream=None):
 
 
 # ---------------------------------------------------------- 8-bit activations
-# These calls run a few microseconds on the GPU, so their checks are one
-# expression an operand (about 0.3 us); only a refused operand is looked at
-# again, for the message.
+# These calls run a few microseconds on the GPU, so what the helpers do before
+# the launch counts: each checks all its operands in one expression (about 0.25
+# us an operand), and only when that fails looks for what to say.
 _a8_state = None
 
 
 def _a8():
     """(rt_dtype of each torch dtype, codes dtype of each format, float32,
-    current raw stream of a device index, current device index)."""
+    current raw stream of a device index, current device index, library)."""
     global _a8_state
     if _a8_state is None:
         import torch
@@ -478,61 +478,65 @@ def _a8():
                 return torch.cuda.current_stream(index).cuda_stream
         current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _a8_state = ({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2},
-                     {FMT_Q8: torch.int8, FMT_E4M3: torch.uint8}, torch.float32, raw, current)
+                     {FMT_Q8: torch.int8, FMT_E4M3: torch.uint8}, torch.float32, raw, current, lib())
     return _a8_state
 
 
-def _a8_refuse(t, dtype, shape, name, index):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{index}")
-
-
-def _a8_ptr(t, dtype, shape, name, index):
-    """Pointer of one operand: type, shape, layout and device checked."""
+def _a8_open(fmt, t, name, coded=False):
+    """What a call starts from: the state above, the codes' dtype, and its first
+    operand's rt_dtype (0 for codes), rows, columns and device index."""
+    state = _a8_state or _a8()
+    types, cdts = state[0], state[1]
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
+        cdt = cdts[fmt]
+        dt = 0 if coded else types[t.dtype]
+        rows, cols = t.shape
+        index = t.get_device()
+        if index >= 0 and (not coded or t.dtype is cdt):
+            return state, cdt, dt, rows, cols, index
+    except (KeyError, TypeError, ValueError, AttributeError):
         pass
-    _a8_refuse(t, dtype, shape, name, index)
-
-
-def _a8_first(t, types, name):
-    """(rt_dtype, rows, columns, device index) of a call's first operand."""
     import torch
+    if not isinstance(fmt, int) or fmt not in cdts:
+        raise ValueError(f"fmt must be 8 (q8) or 3 (e4m3), got {fmt}")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    code = types.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be {' or '.join(map(str, types))}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    rows, cols = t.shape
-    return code, rows, cols, t.get_device()
+    want = (cdts[fmt],) if coded else tuple(types)
+    if t.dtype not in want:
+        raise TypeError(f"{name} must be {' or '.join(map(str, want))}, got {t.dtype}")
+    raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
 
 
-def _a8_codes(fmt, codes):
-    try:
-        return codes[fmt]
-    except (KeyError, TypeError):
-        raise ValueError(f"fmt must be 8 (q8) or 3 (e4m3), got {fmt}") from None
+def _a8_refuse(index, *operands):
+    """Raises for the first of (tensor, dtype, shape, name) that is not as it should be."""
+    import torch
+    for t, dtype, shape, name in operands:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{index}")
+    raise AssertionError("operands are as they should be")
 
 
-def _a8_stream(stream, index, raw, current):
+def _a8_fits(t, dtype, shape, index):
+    return (getattr(t, "dtype", None) is dtype and t.shape == shape and t.get_device() == index and
+            t.is_contiguous())
+
+
+def _a8_stream(stream, index, state):
     """Stream handle; the library launches on the current device, so operands
     of another device, or a stream of another one, are refused."""
-    if current() != index:
-        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{current()}")
+    current = state[4]()
+    if current != index:
+        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{current}")
     if stream is None:
-        return raw(index)
+        return state[3](index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
     return stream.cuda_stream
@@ -546,17 +550,18 @@ def _a8_new(shape, dtype, index):
 def quantize_a8(X, fmt=FMT_Q8, codes=None, scales=None, stream=None):
     """(codes, scales) of the rows of X [M, K] in 8 bits: int8 (fmt 8) or
     e4m3 (fmt 3, as uint8), X float32, float16 or bfloat16."""
-    types, cdts, f32, raw, current = _a8()
-    cdt = _a8_codes(fmt, cdts)
-    dt, M, K, dev = _a8_first(X, types, "X")
+    state, cdt, dt, M, K, index = _a8_open(fmt, X, "X")
+    f32 = state[2]
     if codes is None:
-        codes = _a8_new((M, K), cdt, dev)
+        codes = _a8_new((M, K), cdt, index)
     if scales is None:
-        scales = _a8_new((M,), f32, dev)
-    st = rt_quantize_a8(fmt, dt, _a8_ptr(X, X.dtype, (M, K), "X", dev),
-                        _a8_ptr(codes, cdt, (M, K), "codes", dev),
-                        _a8_ptr(scales, f32, (M,), "scales", dev), M, K,
-                        _a8_stream(stream, dev, raw, current))
+        scales = _a8_new((M,), f32, index)
+    if not (X.is_contiguous() and _a8_fits(codes, cdt, (M, K), index) and
+            _a8_fits(scales, f32, (M,), index)):
+        _a8_refuse(index, (X, X.dtype, (M, K), "X"), (codes, cdt, (M, K), "codes"),
+                   (scales, f32, (M,), "scales"))
+    st = state[5].rt_quantize_a8(fmt, dt, X.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K,
+                                 _a8_stream(stream, index, state))
     if st:
         _check(st, "rt_quantize_a8")
     return codes, scales
@@ -568,23 +573,28 @@ def addnorm_a8(X, gain=None, fmt=FMT_Q8, residual=None, eps=1e-6, H=None, codes=
     gain (fp32 [K] or None), in 8 bits, and h in X's type.  Without a residual
     h is X, and H (None unless given) is only written if given.  H may be X or
     residual itself."""
-    types, cdts, f32, raw, current = _a8()
-    cdt = _a8_codes(fmt, cdts)
-    dt, M, K, dev = _a8_first(X, types, "X")
-    xdt, shape = X.dtype, (M, K)
+    state, cdt, dt, M, K, index = _a8_open(fmt, X, "X")
+    f32, xdt, shape = state[2], X.dtype, (M, K)
     if residual is not None and H is None:
-        H = _a8_new(shape, xdt, dev)
+        H = _a8_new(shape, xdt, index)
     if codes is None:
-        codes = _a8_new(shape, cdt, dev)
+        codes = _a8_new(shape, cdt, index)
     if scales is None:
-        scales = _a8_new((M,), f32, dev)
-    st = rt_addnorm_a8(fmt, dt, _a8_ptr(X, xdt, shape, "X", dev),
-                       None if residual is None else _a8_ptr(residual, xdt, shape, "residual", dev),
-                       None if gain is None else _a8_ptr(gain, f32, (K,), "gain", dev), eps,
-                       None if H is None else _a8_ptr(H, xdt, shape, "H", dev),
-                       _a8_ptr(codes, cdt, shape, "codes", dev),
-                       _a8_ptr(scales, f32, (M,), "scales", dev), M, K,
-                       _a8_stream(stream, dev, raw, current))
+        scales = _a8_new((M,), f32, index)
+    if not (X.is_contiguous() and (residual is None or _a8_fits(residual, xdt, shape, index)) and
+            (gain is None or _a8_fits(gain, f32, (K,), index)) and
+            (H is None or _a8_fits(H, xdt, shape, index)) and _a8_fits(codes, cdt, shape, index) and
+            _a8_fits(scales, f32, (M,), index)):
+        _a8_refuse(index, (X, xdt, shape, "X"),
+                   (X if residual is None else residual, xdt, shape, "residual"),
+                   (scales if gain is None else gain, f32, (M,) if gain is None else (K,), "gain"),
+                   (X if H is None else H, xdt, shape, "H"), (codes, cdt, shape, "codes"),
+                   (scales, f32, (M,), "scales"))
+    st = state[5].rt_addnorm_a8(fmt, dt, X.data_ptr(),
+                                None if residual is None else residual.data_ptr(),
+                                None if gain is None else gain.data_ptr(), eps,
+                                None if H is None else H.data_ptr(), codes.data_ptr(),
+                                scales.data_ptr(), M, K, _a8_stream(stream, index, state))
     if st:
         _check(st, "rt_addnorm_a8")
     return codes, scales, H
@@ -592,20 +602,20 @@ def addnorm_a8(X, gain=None, fmt=FMT_Q8, residual=None, eps=1e-6, H=None, codes=
 
 def gate_a8(U, fmt=FMT_Q8, codes=None, scales=None, stream=None):
     """(codes, scales) of silu(a) * b in 8 bits, U [M, 2F] = a | b."""
-    types, cdts, f32, raw, current = _a8()
-    cdt = _a8_codes(fmt, cdts)
-    dt, M, F2, dev = _a8_first(U, types, "U")
+    state, cdt, dt, M, F2, index = _a8_open(fmt, U, "U")
+    f32, F = state[2], F2 // 2
     if F2 % 2:
         raise ValueError(f"U must hold two halves, got {F2} columns")
-    F = F2 // 2
     if codes is None:
-        codes = _a8_new((M, F), cdt, dev)
+        codes = _a8_new((M, F), cdt, index)
     if scales is None:
-        scales = _a8_new((M,), f32, dev)
-    st = rt_gate_a8(fmt, dt, _a8_ptr(U, U.dtype, (M, F2), "U", dev),
-                    _a8_ptr(codes, cdt, (M, F), "codes", dev),
-                    _a8_ptr(scales, f32, (M,), "scales", dev), M, F,
-                    _a8_stream(stream, dev, raw, current))
+        scales = _a8_new((M,), f32, index)
+    if not (U.is_contiguous() and _a8_fits(codes, cdt, (M, F), index) and
+            _a8_fits(scales, f32, (M,), index)):
+        _a8_refuse(index, (U, U.dtype, (M, F2), "U"), (codes, cdt, (M, F), "codes"),
+                   (scales, f32, (M,), "scales"))
+    st = state[5].rt_gate_a8(fmt, dt, U.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, F,
+                             _a8_stream(stream, index, state))
     if st:
         _check(st, "rt_gate_a8")
     return codes, scales
@@ -613,19 +623,19 @@ def gate_a8(U, fmt=FMT_Q8, codes=None, scales=None, stream=None):
 
 def dequant_a8(fmt, codes, scales, dtype=None, out=None, stream=None):
     """The values code * scale [M, K] in dtype (of out where given, else bfloat16)."""
-    types, cdts, f32, raw, current = _a8()
-    cdt = _a8_codes(fmt, cdts)
-    _, M, K, dev = _a8_first(codes, {cdt: 0}, "codes")
+    state, cdt, _, M, K, index = _a8_open(fmt, codes, "codes", True)
     if out is None:
         import torch
-        out = _a8_new((M, K), dtype or torch.bfloat16, dev)
+        out = _a8_new((M, K), dtype or torch.bfloat16, index)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype {dtype}")
-    dt = _a8_first(out, types, "out")[0]
-    st = rt_dequant_a8(fmt, dt, _a8_ptr(codes, cdt, (M, K), "codes", dev),
-                       _a8_ptr(scales, f32, (M,), "scales", dev),
-                       _a8_ptr(out, out.dtype, (M, K), "out", dev), M, K,
-                       _a8_stream(stream, dev, raw, current))
+    dt = _a8_open(fmt, out, "out")[2]
+    if not (codes.is_contiguous() and _a8_fits(scales, state[2], (M,), index) and
+            _a8_fits(out, out.dtype, (M, K), index)):
+        _a8_refuse(index, (codes, cdt, (M, K), "codes"), (scales, state[2], (M,), "scales"),
+                   (out, out.dtype, (M, K), "out"))
+    st = state[5].rt_dequant_a8(fmt, dt, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), M, K,
+                                _a8_stream(stream, index, state))
     if st:
         _check(st, "rt_dequant_a8")
     return out
@@ -635,24 +645,36 @@ def qgemm_a8(fmt, Xq, x_scales, Wq, w_scales=None, bias=None, Y=None, dtype=None
     """Y [M, N] = (Xq [M, K] @ Wq [N, K]^T) * x_scales [M, 1] * w_scales [1, N] +
     bias [N], both operands int8 (fmt 8) or e4m3 (fmt 3; w_scales may be None).
     Y's type is dtype, or that of Y where given, else float32."""
-    types, cdts, f32, raw, current = _a8()
-    cdt = _a8_codes(fmt, cdts)
-    _, M, K, dev = _a8_first(Xq, {cdt: 0}, "Xq")
-    _, N, _, _ = _a8_first(Wq, {cdt: 0}, "Wq")
+    state, cdt, _, M, K, index = _a8_open(fmt, Xq, "Xq", True)
+    f32 = state[2]
+    try:
+        N = Wq.shape[0]
+    except (AttributeError, IndexError):
+        _a8_open(fmt, Wq, "Wq", True)
+        raise
     if fmt == FMT_Q8 and w_scales is None:
         raise TypeError("q8 weights have row scales")
     if Y is None:
-        Y = _a8_new((M, N), dtype or f32, dev)
+        Y = _a8_new((M, N), dtype or f32, index)
     elif dtype is not None and Y.dtype != dtype:
         raise TypeError(f"Y is {Y.dtype}, dtype {dtype}")
-    dt = _a8_first(Y, types, "Y")[0]
-    st = rt_qgemm_a8(fmt, dt, _a8_ptr(Xq, cdt, (M, K), "Xq", dev),
-                     _a8_ptr(x_scales, f32, (M,), "x_scales", dev),
-                     _a8_ptr(Wq, cdt, (N, K), "Wq", dev),
-                     None if w_scales is None else _a8_ptr(w_scales, f32, (N,), "w_scales", dev),
-                     None if bias is None else _a8_ptr(bias, f32, (N,), "bias", dev),
-                     _a8_ptr(Y, Y.dtype, (M, N), "Y", dev), M, N, K,
-                     _a8_stream(stream, dev, raw, current))
+    ydt = getattr(Y, "dtype", None)
+    dt = state[0].get(ydt)
+    if dt is None:
+        _a8_open(fmt, Y, "Y")
+    if not (Xq.is_contiguous() and _a8_fits(Wq, cdt, (N, K), index) and
+            _a8_fits(x_scales, f32, (M,), index) and
+            (w_scales is None or _a8_fits(w_scales, f32, (N,), index)) and
+            (bias is None or _a8_fits(bias, f32, (N,), index)) and _a8_fits(Y, ydt, (M, N), index)):
+        _a8_refuse(index, (Xq, cdt, (M, K), "Xq"), (x_scales, f32, (M,), "x_scales"),
+                   (Wq, cdt, (N, K), "Wq"),
+                   *(() if w_scales is None else ((w_scales, f32, (N,), "w_scales"),)),
+                   *(() if bias is None else ((bias, f32, (N,), "bias"),)),
+                   (Y, ydt, (M, N), "Y"))
+    st = state[5].rt_qgemm_a8(fmt, dt, Xq.data_ptr(), x_scales.data_ptr(), Wq.data_ptr(),
+                              None if w_scales is None else w_scales.data_ptr(),
+                              None if bias is None else bias.data_ptr(), Y.data_ptr(), M, N, K,
+                              _a8_stream(stream, index, state))
     if st:
         _check(st, "rt_qgemm_a8")
     return Y

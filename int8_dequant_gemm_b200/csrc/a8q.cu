@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 
@@ -94,16 +95,18 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr uint32_t kTinyBits = 0x0D800000u;   // 2^-100: from here on 1 / (max / Q) is finite
 
-// Sum and unsigned maximum over the TPR threads of a row's group; every
+// Unsigned maximum and (SUM) sum over the TPR threads of a row's group; every
 // thread gets both.  TPR > 32: through shared memory, `part` = one slot per
 // warp of the block, two buffers used in turn so that one barrier a call is
 // enough.  A group of whole warps smaller than the block syncs the block: all
 // of a block's groups run the same number of calls.
-template <int TPR>
+template <int TPR, bool SUM>
 __device__ __forceinline__ void row_reduce(float &sum, uint32_t &mx, float2 *part, int &turn) {
     mx = __reduce_max_sync(0xffffffffu, mx);
+    if (SUM) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
     if (TPR > 32) {
         constexpr int kWarps = TPR / 32;
         float2 *buf = part + turn * 32;
@@ -111,64 +114,92 @@ __device__ __forceinline__ void row_reduce(float &sum, uint32_t &mx, float2 *par
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         if (lane == 0) buf[warp] = make_float2(sum, __uint_as_float(mx));
         __syncthreads();
-        const int w0 = warp / kWarps * kWarps;
-        const float2 p = buf[w0 + (lane % kWarps)];
+        const float2 p = buf[warp / kWarps * kWarps + (lane % kWarps)];
         mx = __reduce_max_sync(0xffffffffu, __float_as_uint(p.y));
-        sum = p.x;
+        if (SUM) {
+            sum = p.x;
 #pragma unroll
-        for (int d = kWarps / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            for (int d = kWarps / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
     }
 }
 
-// The integer nearest v / s0 (ties to even), from p within 3e-5 of the
-// quotient.  If p is near a border n + 1/2, the sign of v - (n + 1/2) s0, which
-// one fused multiply-add gives exactly, decides.  `tiny`: s0 may be subnormal,
-// where twice that difference is still a multiple of the smallest subnormal.
-__device__ __forceinline__ float nearest_code(float v, float s0, float p, bool tiny) {
-    const float lo = floorf(p);
-    const float d = tiny ? fmaf(-(2.f * lo + 1.f), s0, 2.f * v) : fmaf(-(lo + 0.5f), s0, v);
-    const float even = 2.f * floorf(0.5f * lo) == lo ? lo : lo + 1.f;
-    const float near = fabsf(p - lo - 0.5f) > 1e-4f ? rintf(p) : d > 0.f ? lo + 1.f : d < 0.f ? lo : even;
-    return fminf(127.f, fmaxf(-127.f, near));
+// a / Q correctly rounded, a = 0 or at least 2^-100: the quotient from the
+// rounded reciprocal, corrected by its exact remainder (Markstein's division).
+template <int FMT>
+__device__ __forceinline__ float over_top(float a) {
+    constexpr float kTop = FMT == kFmtQ8 ? 127.f : 448.f;
+    constexpr float kInv = 1.f / kTop;
+    const float q = a * kInv;
+    return fmaf(fmaf(-q, kTop, a), kInv, q);
 }
 
-// Codes of one 16-byte input vector's values.  int8: v * (1 / s0) is within
-// 3e-5 of the quotient at |code| <= 127 (two roundings of 2^-24), so only a
-// product that close to a rounding border can round to another integer than
-// the quotient; those are decided exactly, and the codes are the host
+// 1.5 * 2^23 + n for an integer |n| <= 128: n in the low mantissa bits.
+constexpr float kMagic = 12582912.f;
+
+// The integer nearest v / s0 (ties to even), in kMagic form, from m = kMagic +
+// the integer nearest an approximation of the quotient that is within 3e-5.
+// The residual r = v - n s0 of one fused multiply-add is exact where it is near
+// s0 / 2 in magnitude; n moves toward its sign if |r| > s0 / 2, or if |r| = s0 / 2
+// and n is odd (magnitudes compare as their bits do).
+__device__ __forceinline__ float nearest_code(float v, float s0, float m) {
+    const float r = fmaf(kMagic - m, s0, v);
+    const uint32_t b = __float_as_uint(m);
+    const bool move = abs_bits(r) + (b & 1u) > __float_as_uint(0.5f * s0);
+    return __uint_as_float(move ? b + (r < 0.f ? 0xFFFFFFFFu : 1u) : b);
+}
+
+// The same for s0 below 2^-100, down to subnormals and 0, where twice the residual
+// against s0 is still a multiple of the smallest subnormal.  A subnormal s0
+// is so coarse that quotients can pass 127: they are held there.
+__device__ __noinline__ float tiny_code(float v, float s0) {
+    if (s0 == 0.f) return kMagic;
+    const float n = rintf(fminf(200.f, fmaxf(-200.f, __fdiv_rn(v, s0))));
+    const float r = fmaf(-2.f * n, s0, 2.f * v);
+    const bool move = abs_bits(r) + (static_cast<int>(n) & 1) > __float_as_uint(s0);
+    return kMagic + fminf(127.f, fmaxf(-127.f, move ? (r < 0.f ? n - 1.f : n + 1.f) : n));
+}
+
+// Codes of one 16-byte input vector's values.  int8: v * inv is within 3e-5 of
+// v / s0 at |code| <= 127 (inv is within 2^-23 of 1 / s0), and one fused
+// multiply-add onto 1.5 * 2^23 rounds it to an integer in the low mantissa bits.
+// Only a product that close to a rounding border can round to another integer
+// than the quotient; those are decided exactly, and the codes are the host
 // quantizer's.  `slow`: s0 is too small for 1 / s0.
 template <int FMT, int N>
 __device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv, bool slow,
                                        uint32_t (&w)[N / 4]) {
     if (FMT == kFmtQ8) {
-        float t[N], edge = 0.f;
+        float m[N], edge = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float p = v[i] * inv;
-            t[i] = rintf(p);
-            edge = fmaxf(edge, fabsf(p - t[i]));
+            m[i] = fmaf(v[i], inv, kMagic);
+            edge = fmaxf(edge, fabsf(fmaf(v[i], inv, kMagic - m[i])));
         }
-        if (slow || edge > 0.49997f) {
+        if (edge > 0.49996f) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float p = slow ? fminf(200.f, fmaxf(-200.f, __fdiv_rn(v[i], s0))) : v[i] * inv;
-                t[i] = s0 > 0.f ? nearest_code(v[i], s0, p, slow) : 0.f;
-            }
+            for (int i = 0; i < N; ++i) m[i] = nearest_code(v[i], s0, m[i]);
+        }
+        if (slow) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) m[i] = tiny_code(v[i], s0);
         }
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            // 1.5 * 2^23 + t holds t in its low byte (two's complement)
             uint32_t b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(t[4 * i + j] + 12582912.f);
+            for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(m[4 * i + j]);
             w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
                                0x5410);
         }
     } else {
         float t[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            t[i] = slow ? (s0 > 0.f ? __fdiv_rn(v[i], s0) : 0.f) : v[i] * inv;
+        for (int i = 0; i < N; ++i) t[i] = v[i] * inv;
+        if (slow) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[i] = s0 > 0.f ? __fdiv_rn(v[i], s0) : 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
             const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]),
@@ -183,17 +214,22 @@ __device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv,
 // a * sigmoid(a) * b = a b / (1 + e^-a).  e^-a overflows to infinity below
 // a = -88.7, where the quotient's true value is below 2^-120 |b|: it becomes 0.
 __device__ __forceinline__ float silu_mul(float a, float b) {
-    return __fdividef(a, 1.f + __expf(-a)) * b;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-a)));
+    return a * r * b;
 }
 
-// One row per group of TPR threads, blockDim.x / TPR rows per block.  Inputs:
-// X [M, K] (gate: [M, 2K], the halves a | b), R [M, K] or NULL, gain [K] or
-// NULL; H [M, K] or NULL receives x + r.  H may be X or R: a thread writes
-// only vectors it has already read.
+// Rows of [M, K] by groups of TPR threads, blockDim.x / TPR rows a block at a
+// time; the blocks stay and walk the rows, and each thread loads its part of
+// the next row before it works on this one, so a row's arithmetic, reduction
+// and stores run under the next row's loads.  Inputs: X [M, K] (gate: [M, 2K],
+// the halves a | b), R [M, K] or NULL, gain [K] or NULL; H [M, K] or NULL
+// receives x + r.  H may be X or R: a row is written after it was read, by the
+// threads that read it.
 template <typename T, int MODE, int FMT, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-    a8_rows_kernel(const T *X, const T *R, const float *__restrict__ gain, float eps, T *H,
-                   uint8_t *__restrict__ codes, float *__restrict__ scales, int M, int K,
+    a8_rows_kernel(const T *X, const T *R, const float *__restrict__ gain, float eps, float inv_k,
+                   T *H, uint8_t *__restrict__ codes, float *__restrict__ scales, int M, int K,
                    DevCtl *ctl) {
     constexpr int V = Vec<T>::n;
     __shared__ float2 part[64];
@@ -204,152 +240,149 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     // wait for this grid.
     pdl_wait_prior_grid();
     const int per_block = blockDim.x / TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / TPR;
     const int t = threadIdx.x % TPR;
-    const bool live = row < M;            // a dead group still takes part in the barriers
-    float v[NV][V];
-    float ss = 0.f;
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-        if (live && k < K) {
-            if (MODE == kModeGate) {
-                const T *p = X + row * 2 * K + k;
-                float a[V], b[V];
-                unpack(*reinterpret_cast<const uint4 *>(p), a, X);
-                unpack(*reinterpret_cast<const uint4 *>(p + K), b, X);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] = silu_mul(a[j], b[j]);
-            } else {
-                unpack(*reinterpret_cast<const uint4 *>(X + row * K + k), v[i], X);
-                if (MODE == kModeNorm && R) {
-                    float r[V];
-                    unpack(*reinterpret_cast<const uint4 *>(R + row * K + k), r, X);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) v[i][j] += r[j];
-                }
-            }
-        }
-    }
-    if (MODE == kModeNorm && H) {
-        // rounded once to the stream's type; the norm below is of the fp32 sum
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / TPR;
+
+    uint4 in0[NV], in1[NV];               // x, or a; the residual, or b
+    const auto load = [&](int64_t at) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (live && k < K) *reinterpret_cast<uint4 *>(H + row * K + k) = pack(v[i], X);
+            const bool have = at < M && k < K;
+            const T *p = X + (MODE == kModeGate ? at * 2 * K : at * K) + k;
+            in0[i] = have ? *reinterpret_cast<const uint4 *>(p) : zero;
+            if (MODE == kModeGate) in1[i] = have ? *reinterpret_cast<const uint4 *>(p + K) : zero;
+            if (MODE == kModeNorm && R)
+                in1[i] = have ? *reinterpret_cast<const uint4 *>(R + at * K + k) : zero;
         }
-    }
+    };
+    load(row);
+    // the block's groups make the same number of turns: they share barriers
+    for (int64_t lead = row - threadIdx.x / TPR; lead < M; lead += step, row += step) {
+        const bool live = row < M;
+        float v[NV][V];
+        float ss = 0.f;
+        uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
-        if (MODE == kModeNorm) {
+        for (int i = 0; i < NV; ++i) {
+            unpack(in0[i], v[i], X);
+            if (MODE == kModeGate || (MODE == kModeNorm && R)) {
+                float b[V];
+                unpack(in1[i], b, X);
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-            if (gain && k < K) {
+                for (int j = 0; j < V; ++j)
+                    v[i][j] = MODE == kModeGate ? silu_mul(v[i][j], b[j]) : v[i][j] + b[j];
+            }
+        }
+        load(row + step);
+        if (MODE == kModeNorm && H) {
+            // rounded once to the stream's type; the norm below is of the fp32 sum
 #pragma unroll
-                for (int j = 0; j < V; j += 4) {
-                    const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
-                    const float gg[4] = {g.x, g.y, g.z, g.w};
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * TPR + t) * V;
+                if (live && k < K) *reinterpret_cast<uint4 *>(H + row * K + k) = pack(v[i], X);
+            }
+        }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx = max(mx, abs_bits(v[i][j + q] * gg[q]));
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (MODE == kModeNorm) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+                if (gain && k < K) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 4) {
+                        const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
+                        const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx = max(mx, abs_bits(v[i][j + q] * gg[q]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) mx = max(mx, abs_bits(v[i][j]));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) mx = max(mx, abs_bits(v[i][j]));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) mx = max(mx, abs_bits(v[i][j]));
         }
-    }
-    row_reduce<TPR>(ss, mx, part, turn);
-    float mul = 1.f;                      // scale = s0 * mul
-    if (MODE == kModeNorm) {
-        mul = __frsqrt_rn(ss / static_cast<float>(K) + eps);
-        // The squares or h * gain have left fp32's range, or the products are
-        // so small that their quotients would lose digits: the row once more
-        // as y itself, from h * 2^-80 where the squares overflowed.  A group
-        // agrees on this; groups that share barriers take the block's vote.
-        const bool redo = live && (!(ss <= FLT_MAX) || mx >= kInfBits || mx < kTinyBits);
-        const bool any = (TPR == 32 || TPR >= 256) ? redo : __syncthreads_or(redo) != 0;
-        if (any) {
-            const float f = ss <= FLT_MAX ? 1.f : 0x1p-80f;
-            float s2 = 0.f, none = 0.f;
-            uint32_t m2 = 0;
+        row_reduce<TPR, MODE == kModeNorm>(ss, mx, part, turn);
+        float mul = 1.f;                  // scale = s0 * mul
+        if (MODE == kModeNorm) {
+            mul = rsqrtf(fmaf(ss, inv_k, eps));
+            // The squares or h * gain have left fp32's range, or the products
+            // are so small that their quotients would lose digits: the row once
+            // more as y itself, from h * 2^-80 where the squares overflowed.  A
+            // group agrees on this; groups that share barriers take the block's
+            // vote.
+            const bool redo = live && (!(ss <= FLT_MAX) || mx >= kInfBits || mx < kTinyBits);
+            const bool any = (TPR == 32 || TPR >= 256) ? redo : __syncthreads_or(redo) != 0;
+            if (any) {
+                const float f = ss <= FLT_MAX ? 1.f : 0x1p-80f;
+                float s2 = 0.f, none = 0.f;
+                uint32_t m2 = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) s2 = fmaf(v[i][j] * f, v[i][j] * f, s2);
-            row_reduce<TPR>(s2, m2, part, turn);
-            const float r2 = __frsqrt_rn(s2 / static_cast<float>(K) + eps * f * f);
-            m2 = 0;
+                    for (int j = 0; j < V; ++j) s2 = fmaf(v[i][j] * f, v[i][j] * f, s2);
+                row_reduce<TPR, true>(s2, m2, part, turn);
+                const float r2 = rsqrtf(fmaf(s2, inv_k, eps * f * f));
+                m2 = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int k = (i * TPR + t) * V;
+                for (int i = 0; i < NV; ++i) {
+                    const int k = (i * TPR + t) * V;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (redo) v[i][j] = v[i][j] * f * r2;
-                    m2 = max(m2, abs_bits(v[i][j] * (gain && k < K ? __ldg(gain + k + j) : 1.f)));
+                    for (int j = 0; j < V; ++j) {
+                        if (redo) v[i][j] = v[i][j] * f * r2;
+                        m2 = max(m2,
+                                 abs_bits(v[i][j] * (gain && k < K ? __ldg(gain + k + j) : 1.f)));
+                    }
+                }
+                row_reduce<TPR, false>(none, m2, part, turn);
+                if (redo) {
+                    mx = m2;
+                    mul = 1.f;
                 }
             }
-            row_reduce<TPR>(none, m2, part, turn);
-            if (redo) {
-                mx = m2;
-                mul = 1.f;
-            }
         }
-    }
-    if (!live) return;
-    const float amax = __uint_as_float(mx);
-    constexpr float kTop = FMT == kFmtQ8 ? 127.f : 448.f;
-    if (mx >= kInfBits) {
-        // a value that is not finite: the row has no scale; its codes are 0
-        // and the product gives NaN for it, and for it alone
+        if (!live) continue;
+        // A value that is not finite: the row has no scale; its codes are 0 and
+        // the product gives NaN for it, and for it alone.
+        const bool bad = mx >= kInfBits;
+        const float amax = __uint_as_float(mx);
+        const bool slow = mx < kTinyBits;
+        const float s0 = slow ? __fdiv_rn(amax, FMT == kFmtQ8 ? 127.f : 448.f) : over_top<FMT>(amax);
+        const float inv = slow ? 0.f : __fdividef(1.f, s0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (k < K) {
-                if (V == 4)
-                    *reinterpret_cast<uint32_t *>(codes + row * K + k) = 0u;
-                else
-                    *reinterpret_cast<uint2 *>(codes + row * K + k) = make_uint2(0u, 0u);
+            if (k >= K) continue;
+            if (MODE == kModeNorm) {
+#pragma unroll
+                for (int j = 0; j < V && gain; j += 4) {
+                    const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
+                    v[i][j] *= g.x;
+                    v[i][j + 1] *= g.y;
+                    v[i][j + 2] *= g.z;
+                    v[i][j + 3] *= g.w;
+                }
             }
+            uint32_t w[V / 4];
+            encode<FMT, V>(v[i], s0, inv, slow, w);
+            if (bad) w[0] = w[V / 4 - 1] = 0u;
+            if (V == 4)
+                *reinterpret_cast<uint32_t *>(codes + row * K + k) = w[0];
+            else
+                *reinterpret_cast<uint2 *>(codes + row * K + k) = make_uint2(w[0], w[V / 4 - 1]);
         }
         if (t == 0) {
-            scales[row] = __uint_as_float(0x7FC00000u);
-            atomicOr(&ctl->status, 1u << kStatusRange);
+            scales[row] = bad ? __uint_as_float(0x7FC00000u) : s0 * mul;
+            if (bad) atomicOr(&ctl->status, 1u << kStatusRange);
         }
-        return;
     }
-    const float s0 = __fdiv_rn(amax, kTop);
-    const bool slow = mx < kTinyBits;
-    const float inv = slow ? 0.f : __fdiv_rn(1.f, s0);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
-        if (k >= K) continue;
-        if (MODE == kModeNorm) {
-#pragma unroll
-            for (int j = 0; j < V && gain; j += 4) {
-                const float4 g = __ldg(reinterpret_cast<const float4 *>(gain + k + j));
-                v[i][j] *= g.x;
-                v[i][j + 1] *= g.y;
-                v[i][j + 2] *= g.z;
-                v[i][j + 3] *= g.w;
-            }
-        }
-        uint32_t w[V / 4];
-        encode<FMT, V>(v[i], s0, inv, slow, w);
-        if (V == 4)
-            *reinterpret_cast<uint32_t *>(codes + row * K + k) = w[0];
-        else
-            *reinterpret_cast<uint2 *>(codes + row * K + k) = make_uint2(w[0], w[V / 4 - 1]);
-    }
-    if (t == 0) scales[row] = s0 * mul;
 }
 
 // Values of 8-bit rows: code * scale in fp32, rounded once to the type.
@@ -405,7 +438,7 @@ cudaError_t launch_pdl(const void *fn, unsigned grid, unsigned block, void **arg
 struct RowArgs {
     const void *X, *R;
     const float *gain;
-    float eps;
+    float eps, inv_k;
     void *H;
     uint8_t *codes;
     float *scales;
@@ -413,35 +446,73 @@ struct RowArgs {
     DevCtl *ctl;
 };
 
+// Blocks of `kernel` that the current device holds at once (cached).
+template <typename Kernel>
+int resident_blocks(Kernel kernel, int threads, std::atomic<int> (&cache)[kMaxDevices]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+    int n = cache[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    int per = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) != cudaSuccess ||
+        per < 1) {
+        cudaGetLastError();
+        per = 1;
+    }
+    n = per * sm_count();
+    cache[dev].store(n, std::memory_order_release);
+    return n;
+}
+
 template <typename T, int MODE, int FMT, int TPR, int NV>
 cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
     constexpr int kBlock = TPR < 256 ? 256 : TPR;
     constexpr int kRows = kBlock / TPR;
     const T *X = static_cast<const T *>(a.X), *R = static_cast<const T *>(a.R);
     T *H = static_cast<T *>(a.H);
-    void *args[] = {&X, &R, &a.gain, &a.eps, &H, &a.codes, &a.scales, &a.M, &a.K, &a.ctl};
-    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
-    // few rows: no more threads than they need
-    const unsigned block = a.M < kRows ? static_cast<unsigned>(a.M * TPR) : kBlock;
-    return launch_pdl(reinterpret_cast<const void *>(a8_rows_kernel<T, MODE, FMT, TPR, NV>), grid,
-                      block, args, s);
+    void *args[] = {&X, &R, &a.gain, &a.eps, &a.inv_k, &H, &a.codes, &a.scales, &a.M, &a.K, &a.ctl};
+    const auto kernel = a8_rows_kernel<T, MODE, FMT, TPR, NV>;
+    static std::atomic<int> resident[kMaxDevices];
+    const int most = resident_blocks(kernel, kBlock, resident);
+    const int64_t want = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
+    unsigned grid = static_cast<unsigned>(want < most ? want : most), block = kBlock;
+    if (kRows > 1 && want < 2 * sm_count()) {      // few rows: blocks of fewer rows, on more SMs
+        const int rows = static_cast<int>((a.M + 2 * sm_count() - 1) / (2 * sm_count()));
+        block = static_cast<unsigned>(rows * TPR);
+        grid = static_cast<unsigned>((a.M + rows - 1) / rows);
+    }
+    return launch_pdl(reinterpret_cast<const void *>(kernel), grid, block, args, s);
 }
 
-// Threads a row: the fewest whose vectors fit in 16 values (fp32) or 32
-// values (16-bit types) a thread.
-template <typename T, int MODE, int FMT>
-cudaError_t launch_rows_k(const RowArgs &a, cudaStream_t s) {
-    const int vecs = a.K / Vec<T>::n;
-    constexpr int NV = 4;
-    if (vecs <= 32) return launch_rows<T, MODE, FMT, 32, 1>(a, s);
-    if (vecs <= 64) return launch_rows<T, MODE, FMT, 32, 2>(a, s);
+// The narrowest group of 32 to 1024 threads whose NV vectors a thread hold a row.
+template <typename T, int MODE, int FMT, int NV>
+cudaError_t launch_rows_nv(const RowArgs &a, int vecs, cudaStream_t s) {
     if (vecs <= 32 * NV) return launch_rows<T, MODE, FMT, 32, NV>(a, s);
     if (vecs <= 64 * NV) return launch_rows<T, MODE, FMT, 64, NV>(a, s);
     if (vecs <= 128 * NV) return launch_rows<T, MODE, FMT, 128, NV>(a, s);
     if (vecs <= 256 * NV) return launch_rows<T, MODE, FMT, 256, NV>(a, s);
-    if (vecs <= 512 * NV) return launch_rows<T, MODE, FMT, 512, NV>(a, s);
-    if (Vec<T>::n == 8 || vecs <= 1024 * NV) return launch_rows<T, MODE, FMT, 1024, NV>(a, s);
-    return launch_rows<T, MODE, FMT, 1024, Vec<T>::n == 4 ? 8 : NV>(a, s);   // up to kMaxRowK
+    if (NV == 1 || vecs <= 512 * NV) return launch_rows<T, MODE, FMT, 512, NV>(a, s);
+    return launch_rows<T, MODE, FMT, 1024, NV>(a, s);
+}
+
+// Vectors a thread.  Few rows: 1, for the shortest chain (80 x 512 bf16 norm: 1.7
+// us, with 2 it takes 2.4).  Many rows: what keeps most bytes in flight for the
+// registers it takes.  16-bit types 2: 65536 x 2048 bf16 gate 110 us (1: 122, 4:
+// 111), norm 148 (1: 156, 4: 172).  fp32 quantization 4: 65536 x 512 26 us (2: 29,
+// 1: 37); gate 2: 4096 x 2048 12.8 us (4: 13.7); norm 1 up to 128 vectors, then
+// 2: 65536 x 512 68 us (2: 72, 4: 92), 65536 x 2048 276 us (4: 346).  The longest
+// rows take what 1024 threads need.
+template <typename T, int MODE, int FMT>
+cudaError_t launch_rows_k(const RowArgs &a, cudaStream_t s) {
+    constexpr bool kWide = Vec<T>::n == 4;            // fp32
+    constexpr int kMany = kWide && MODE == kModeQuant ? 4 : 2;
+    const int vecs = a.K / Vec<T>::n;
+    const bool few = a.M <= 8 * sm_count();
+    if (vecs <= 512 && (few || (kWide && MODE == kModeNorm && vecs <= 128)))
+        return launch_rows_nv<T, MODE, FMT, 1>(a, vecs, s);
+    if (vecs <= 1024 * kMany) return launch_rows_nv<T, MODE, FMT, kMany>(a, vecs, s);
+    if (kMany < 4 && vecs <= 4096) return launch_rows<T, MODE, FMT, 1024, 4>(a, s);
+    return launch_rows<T, MODE, FMT, 1024, kWide ? 8 : 4>(a, s);     // up to kMaxRowK
 }
 
 template <typename T, int MODE>
@@ -475,19 +546,19 @@ cudaError_t launch_values(int fmt, const uint8_t *codes, const float *scales, T 
 cudaError_t launch_quantize_a8(int fmt, int dtype, const void *X, uint8_t *codes, float *scales,
                                int M, int K, DevCtl *ctl, cudaStream_t s) {
     return launch_rows_t<kModeQuant>(
-        fmt, dtype, {X, nullptr, nullptr, 0.f, nullptr, codes, scales, M, K, ctl}, s);
+        fmt, dtype, {X, nullptr, nullptr, 0.f, 0.f, nullptr, codes, scales, M, K, ctl}, s);
 }
 
 cudaError_t launch_addnorm_a8(int fmt, int dtype, const void *X, const void *R, const float *gain,
                               float eps, void *H, uint8_t *codes, float *scales, int M, int K,
                               DevCtl *ctl, cudaStream_t s) {
-    return launch_rows_t<kModeNorm>(fmt, dtype, {X, R, gain, eps, H, codes, scales, M, K, ctl}, s);
+    return launch_rows_t<kModeNorm>(fmt, dtype, {X, R, gain, eps, 1.f / static_cast<float>(K), H, codes, scales, M, K, ctl}, s);
 }
 
 cudaError_t launch_gate_a8(int fmt, int dtype, const void *U, uint8_t *codes, float *scales, int M,
                            int F, DevCtl *ctl, cudaStream_t s) {
     return launch_rows_t<kModeGate>(
-        fmt, dtype, {U, nullptr, nullptr, 0.f, nullptr, codes, scales, M, F, ctl}, s);
+        fmt, dtype, {U, nullptr, nullptr, 0.f, 0.f, nullptr, codes, scales, M, F, ctl}, s);
 }
 
 cudaError_t launch_dequant_a8(int fmt, int dtype, const uint8_t *codes, const float *scales,
