@@ -165,10 +165,12 @@ __device__ __noinline__ float tiny_code(float v, float s0) {
 // multiply-add onto 1.5 * 2^23 rounds it to an integer in the low mantissa bits.
 // Only a product that close to a rounding border can round to another integer
 // than the quotient; those are decided exactly, and the codes are the host
-// quantizer's.  `slow`: s0 is too small for 1 / s0.
+// quantizer's.  e4m3: v * (inv + inv_lo), inv + inv_lo = Q / max|v| to about
+// 2^-45, so that the quotient is rounded once before it is rounded to 8 bits.
+// `slow`: s0 is too small for 1 / s0.
 template <int FMT, int N>
-__device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv, bool slow,
-                                       uint32_t (&w)[N / 4]) {
+__device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv, float inv_lo,
+                                       bool slow, uint32_t (&w)[N / 4]) {
     if (FMT == kFmtQ8) {
         float m[N], edge = 0.f;
 #pragma unroll
@@ -195,7 +197,7 @@ __device__ __forceinline__ void encode(const float (&v)[N], float s0, float inv,
     } else {
         float t[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = v[i] * inv;
+        for (int i = 0; i < N; ++i) t[i] = fmaf(v[i], inv, v[i] * inv_lo);
         if (slow) {
 #pragma unroll
             for (int i = 0; i < N; ++i) t[i] = s0 > 0.f ? __fdiv_rn(v[i], s0) : 0.f;
@@ -355,7 +357,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
         const float amax = __uint_as_float(mx);
         const bool slow = mx < kTinyBits;
         const float s0 = slow ? __fdiv_rn(amax, FMT == kFmtQ8 ? 127.f : 448.f) : over_top<FMT>(amax);
-        const float inv = slow ? 0.f : __fdividef(1.f, s0);
+        float inv = slow ? 0.f : __fdividef(1.f, s0), inv_lo = 0.f;
+        if (FMT == kFmtE4M3 && !slow) {
+            // the rest of Q / amax beyond inv, from its exact remainder
+            inv = fmaf(fmaf(-inv, s0, 1.f), inv, inv);
+            inv_lo = fmaf(-inv, amax, 448.f) * (inv * (1.f / 448.f));
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
                 }
             }
             uint32_t w[V / 4];
-            encode<FMT, V>(v[i], s0, inv, slow, w);
+            encode<FMT, V>(v[i], s0, inv, inv_lo, slow, w);
             if (bad) w[0] = w[V / 4 - 1] = 0u;
             if (V == 4)
                 *reinterpret_cast<uint32_t *>(codes + row * K + k) = w[0];
