@@ -165,7 +165,7 @@ def lib() -> ctypes.CDLL:
     L.rt_qgemm_a8.restype = _i32
     L.rt_qgemm_a8.argtypes = [_i32, _i32, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]
     L.rt_qgemm_a8_plan.restype = _i32
-    L.rt_qgemm_a8_plan.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
+    L.rt_qgemm_a8_plan.argtypes = [_i32, _i64, _i64, _i64, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
     _lib = L
     return L
 
@@ -316,8 +316,8 @@ def rt_qgemm_a8(fmt, dtype, Xq, x_scales, Wq, w_scales, bias, Y, M, N, K, stream
     return lib().rt_qgemm_a8(fmt, dtype, Xq, x_scales, Wq, w_scales, bias, Y, M, N, K, stream)
 
 
-def rt_qgemm_a8_plan(M, N, K, tile_rows, split) -> int:
-    return lib().rt_qgemm_a8_plan(M, N, K, tile_rows, split)
+def rt_qgemm_a8_plan(fmt, M, N, K, tile_rows, split) -> int:
+    return lib().rt_qgemm_a8_plan(fmt, M, N, K, tile_rows, split)
 
 
 # ------------------------------------------------------- torch-level helpers
@@ -680,15 +680,17 @@ def qgemm_a8(fmt, Xq, x_scales, Wq, w_scales=None, bias=None, Y=None, dtype=None
     return Y
 
 
-def a8_plan(M, N, K):
-    """How qgemm_a8 tiles these sizes on the current device: a dict of `rows`
+def a8_plan(M, N, K, fmt=FMT_Q8):
+    """How qgemm_a8 computes these sizes on the current device: a dict of `rows`
     (activation rows a tile), `split` (CTAs that share a tile's K), `pair`
-    (CTA pairs share an MMA) and `walk` (CTAs walk several tiles); None for
-    sizes it refuses."""
+    (CTA pairs share an MMA), `walk` (CTAs walk several tiles) and `cores`
+    (CUDA cores, no tensor cores); None for sizes it refuses."""
     rows, split = _i32(), _i32()
-    r = rt_qgemm_a8_plan(M, N, K, ctypes.byref(rows), ctypes.byref(split))
-    return None if r < 0 else {"rows": rows.value, "split": split.value, "pair": bool(r & 1),
-                               "walk": not r & 2}
+    r = rt_qgemm_a8_plan(fmt, M, N, K, ctypes.byref(rows), ctypes.byref(split))
+    if r < 0:
+        return None
+    return {"rows": rows.value, "split": split.value, "pair": bool(r & 1), "walk": not r & 6,
+            "cores": bool(r & 4)}
 
 
 @dataclass

@@ -696,14 +696,14 @@ int sm_count() {
 // handshakes; in a walk of tiles the shorter of load and epilogue hides by 70 %.  Fitted to 1.7 thousand timings of M = 1 to 4096 against eight
 // weight shapes from 512 x 512 to 8192 x 8192; over those shapes the plan taken
 // is on average 1.8 % slower than the best of them, at most 25 %.
-A8Plan plan_a8(int M, int N, int K, int sms) {
+A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
     const int nkb = (K + kKBytes - 1) / kKBytes;
     const int n_o = static_cast<int>((static_cast<int64_t>(N) + kTileRows - 1) / kTileRows);
     const int n_op = (n_o + 1) / 2;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const auto rows_us = [&](int rows, int kb) { return 0.001235f * static_cast<float>(rows) * kb; };
     const auto epi_us = [](int bn) { return 0.47f + 0.0067f * static_cast<float>(bn); };
-    A8Plan best = {16, 1, 0, 1};
+    A8Plan best = {16, 1, 0, 1, 0};
     float least = 1e30f;
     const auto offer = [&](const A8Plan &p, float us) {
         if (us < least) {
@@ -720,7 +720,7 @@ A8Plan plan_a8(int M, int N, int K, int sms) {
             constexpr float kCluster[4] = {0.f, 0.42f, 0.26f, 0.61f};
             if (split > nkb || tiles * split > 6 * sms) break;
             const float per = static_cast<float>(up(tiles * split, sms));
-            offer({bn, split, 0, 1},
+            offer({bn, split, 0, 1, 0},
                   per * rows_us(kTileRows + bn, (nkb + split - 1) / split) + 0.34f * (per - 1.f) +
                       epi_us(bn) * (split > 1 ? 2.34f : 1.f) + kCluster[log]);
         }
@@ -731,16 +731,31 @@ A8Plan plan_a8(int M, int N, int K, int sms) {
             const int64_t tiles = (pair ? n_op : n_o) * up(std::max(M, 1), bn);
             const float per = static_cast<float>(up(tiles, pair ? sms / 2 : sms));
             const float load = rows_us(kTileRows + (pair ? bn / 2 : bn), nkb), epi = epi_us(bn);
-            offer({bn, 1, pair, 0},
+            offer({bn, 1, pair, 0, 0},
                   load + (per - 1.f) * (std::max(load, epi) + 0.3f * std::min(load, epi)) + epi +
                       (pair ? 0.9f : 0.f));
         }
+    // A few rows on the CUDA cores: 1.55 us less to set up; 0.08 us a 512-byte step
+    // of K, and a byte of weights costs its load or its arithmetic.  The tensor
+    // path takes weights from HBM at 5.4 TB/s at most.  Measured, us, CUDA cores
+    // and tensor cores: M = 1, int8, 512 x 512: 1.5 and 3.5, 512 x 2048 (K): 2.0 and
+    // 4.8, 8192 x 8192: 12.2 and 15.2; M = 8, 4096 x 4096: 9.1 and 6.2; e4m3, M = 1,
+    // 8192 x 8192: 17.1 and 15.6.
+    if (M >= 1 && M <= 8) {
+        const float mbytes = 1e-6f * static_cast<float>(N) * static_cast<float>(K);
+        const float byte_us = fmt == kFmtQ8 ? 0.12f + 0.031f * M : 0.14f + 0.089f * M;
+        least = std::max(least, mbytes / 5.4f);
+        offer({8, 1, 0, 0, K <= 512 && N >= 2048 ? 4 : 1},
+              0.08f * static_cast<float>(up(K, 512)) + byte_us * mbytes - 1.55f);
+    }
     return best;
 }
 
 cudaError_t launch_qgemm_a8(const A8Plan &plan, int fmt, int dtype, const void *Xq, const float *xs,
                             const void *Wq, const float *wsc, const float *bias, void *Y, int M,
                             int N, int K, DevCtl *ctl, cudaStream_t s) {
+    if (plan.few)
+        return launch_qgemm_a8_few(plan.few, fmt, dtype, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
     return fmt == kFmtQ8
                ? launch_a8_y<kFmtQ8>(plan, dtype, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s)
                : launch_a8_y<kFmtE4M3>(plan, dtype, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);

@@ -148,19 +148,19 @@ rt_status rt_qgemm_a8(int fmt, int dtype, const void *Xq, const float *x_scales,
     rt_status st = rtq::device_ctl(&ctl);
     if (st != RT_OK) return st;
     const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-    return from_cuda(rtq::launch_qgemm_a8(rtq::plan_a8(m, n, k, rtq::sm_count()), fmt, dtype, Xq,
+    return from_cuda(rtq::launch_qgemm_a8(rtq::plan_a8(fmt, m, n, k, rtq::sm_count()), fmt, dtype, Xq,
                                           x_scales, Wq, w_scales, bias, Y, m, n, k, ctl,
                                           static_cast<cudaStream_t>(stream)));
 }
 
-int rt_qgemm_a8_plan(int64_t M, int64_t N, int64_t K, int *tile_rows, int *split) {
-    if (M < 0 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K % 16 != 0 || K > kMaxSumK)
+int rt_qgemm_a8_plan(int fmt, int64_t M, int64_t N, int64_t K, int *tile_rows, int *split) {
+    if (!fmt8_valid(fmt) || M < 0 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K % 16 != 0 || K > kMaxSumK)
         return -1;
-    const rtq::A8Plan p = rtq::plan_a8(static_cast<int>(M), static_cast<int>(N),
+    const rtq::A8Plan p = rtq::plan_a8(fmt, static_cast<int>(M), static_cast<int>(N),
                                        static_cast<int>(K), rtq::sm_count());
     if (tile_rows) *tile_rows = p.bn;
     if (split) *split = p.split;
-    return p.pair | (p.small << 1);
+    return p.few ? 4 : p.pair | (p.small << 1);
 }
 
 }  // extern "C"

@@ -215,15 +215,22 @@ cudaError_t launch_dequant_a8(int fmt, int dtype, const uint8_t *codes, const fl
 // The tile plan of an 8-bit product: activation rows per tile, K slices
 // (CTAs of a cluster that share a tile's K), whether CTA pairs share one MMA,
 // and whether CTAs of 192 threads take one tile each (bn <= 128; always so
-// with a split).  plan_a8 picks it from the shape and the SM count.
+// with a split).  few > 0: CUDA cores instead, that many weight rows a warp.
+// plan_a8 picks it from format, shape and SM count.
 struct A8Plan {
-    int bn, split, pair, small;
+    int bn, split, pair, small, few;
 };
 int sm_count();                        // of the current device (cached)
-A8Plan plan_a8(int M, int N, int K, int sms);
+A8Plan plan_a8(int fmt, int M, int N, int K, int sms);
 cudaError_t launch_qgemm_a8(const A8Plan &plan, int fmt, int dtype, const void *Xq, const float *xs,
                             const void *Wq, const float *wsc, const float *bias, void *Y, int M,
                             int N, int K, DevCtl *ctl, cudaStream_t s);
+
+// The same product for M <= 8 on the CUDA cores, rw = 1 or 4 weight rows a warp
+// (a8v.cu).
+cudaError_t launch_qgemm_a8_few(int rw, int fmt, int dtype, const void *Xq, const float *xs,
+                                const void *Wq, const float *wsc, const float *bias, void *Y, int M,
+                                int N, int K, DevCtl *ctl, cudaStream_t s);
 
 // dequantization exports (same __device__ routines as the GEMMs)
 cudaError_t launch_dequant_q4_f32(const uint8_t *Wq, const uint16_t *SM, float *W, int N, int K,

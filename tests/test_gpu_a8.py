@@ -281,7 +281,8 @@ SIZES = [(1, 1, 16), (1, 4096, 512), (2, 7, 32), (15, 130, 144), (16, 128, 128),
          (128, 129, 4112), (129, 300, 272), (130, 1, 16), (200, 2048, 512), (256, 256, 1024),
          (257, 513, 640), (300, 512, 2048), (513, 384, 128), (1000, 1003, 1040), (1024, 4096, 512),
          (2049, 512, 2064), (4096, 512, 512), (2500, 1000, 512), (3001, 2000, 400),
-         (5003, 1003, 1040), (4100, 2200, 2048), (9000, 515, 256), (7, 5000, 2048), (520, 4999, 1024)]
+         (5003, 1003, 1040), (4100, 2200, 2048), (9000, 515, 256), (9, 5000, 2048), (520, 4999, 1024),
+         (3, 4097, 512), (4, 131, 8208), (5, 512, 2048), (8, 515, 528), (8, 4100, 4096), (2, 6001, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -301,10 +302,12 @@ def test_product(rtq, M, N, K, fmt):
 
 
 def test_product_sizes_take_every_plan(rtq):
-    plans = [rtq.a8_plan(*n) for n in SIZES]
-    assert {p["split"] for p in plans} >= {1, 2, 4, 8}
-    assert any(not p["walk"] and p["split"] == 1 for p in plans)
-    assert any(p["walk"] and p["pair"] for p in plans) and any(p["walk"] and not p["pair"] for p in plans)
+    for fmt in (Q8, E4M3):
+        plans = [rtq.a8_plan(*n, fmt) for n in SIZES]
+        assert any(p["cores"] for p in plans) and {p["split"] for p in plans} >= {1, 2, 4, 8}
+        assert any(not (p["walk"] or p["cores"]) and p["split"] == 1 for p in plans)
+        assert any(p["walk"] and p["pair"] for p in plans)
+        assert any(p["walk"] and not p["pair"] for p in plans)
 
 
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
