@@ -48,9 +48,8 @@ constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights a stage
 // SM's registers and shared memory, so the next kernel's CTA starts beside it).
 constexpr int epi_warp0(int G) { return G == 1 ? 2 : 4; }
 constexpr int cta_threads(int G) { return (epi_warp0(G) + 4 * G) * 32; }
-constexpr int kMaxBn = 256, kMaxStages = 8;
+constexpr int kMaxStages = 8;
 constexpr int kBand = 8;                           // activation tiles walked together
-constexpr uint32_t kEpiBar = 1;                    // named barriers: an epilogue set (1, 2)
 constexpr uint16_t kBoth = 3;                      // multicast mask: both CTAs of a pair
 constexpr int kSmemMax = 200 * 1024;               // ring of stages
 constexpr int kSmemSmall = 100 * 1024;             // the same for G = 1
@@ -63,8 +62,8 @@ struct A8Args {
     int n_o, n_m;            // weight tiles, activation tiles
     int acc_cols;
     int alt;                 // two epilogue sets take turns
-    int tail_off;            // after the ring: activation scales [4][kMaxBn],
-                             // barriers and words
+    int tail_off;            // after the ring: each epilogue warp's activation
+                             // scales [16][kWarpRows], barriers and words
 };
 
 __host__ __device__ constexpr int stage_bytes(int bn, int pair) {
@@ -77,7 +76,8 @@ __host__ inline int ring_bytes(const A8Args &a, int pair) {
     const int red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
     return ring > red ? ring : red;
 }
-constexpr int kTailBytes = 4 * kMaxBn * 4 + (2 * kMaxStages + 5) * 8 + 16;
+constexpr int kWarpRows = 128;                     // activation rows of a tile an epilogue warp takes
+constexpr int kTailBytes = 16 * kWarpRows * 4 + (2 * kMaxStages + 5) * 8 + 16;
 
 // Instruction descriptors (A and B K-major): accumulator s32 (2) or f32 (1),
 // operand type 1 = s8 of kind::i8, 0 = e4m3 of kind::f8f6f4.
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     const uint32_t base = smem_addr(smem);
     uint8_t *tail = smem + a.tail_off;
     float *xs_s = reinterpret_cast<float *>(tail);
-    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 4 * kMaxBn * 4);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 16 * kWarpRows * 4);
     uint64_t *empty = full + kMaxStages;
     uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -425,19 +425,23 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         const int ew = warp - kEpiWarp0;
         const int set = a.alt ? ew >> 3 : 0, groups = a.alt ? G / 2 : G;
         const int h = a.alt ? (ew >> 2) & 1 : ew >> 2;
-        const int et = (static_cast<int>(threadIdx.x) - kEpiWarp0 * 32) & (groups * 128 - 1);
         const int turn = a.alt ? 2 : 1, chunk_step = 2 * kChunk * groups;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
         YT *const Y = static_cast<YT *>(a.Y);
         uint32_t nf = 0;                     // NaN once an output is not finite
-        // the next tile's scales and bias are loaded while this one is stored:
-        // activation row et's scale by thread et, this lane's by every warp
-        float x_next = 0.f, w_next = 1.f, b_next = 0.f;
+        // The next tile's scales and bias are loaded while this one is stored.  Each
+        // warp keeps the scales of its own activation rows: the warps share no
+        // barrier, which a warp whose wait gave up would not come to.
+        float *const xs_w = xs_s + ew * kWarpRows;
+        float x_next[kWarpRows / 32] = {}, w_next = 1.f, b_next = 0.f;
         auto fetch = [&](int t) {
             if (split > 1 || t >= n_tiles) return;
             const TileAt at(t, a.n_m, a.n_o);
-            const int m = at.m * a.bn + et;
-            if (et < a.bn && m < a.M) x_next = __ldg(a.xs + m);
+#pragma unroll
+            for (int i = 0; i < kWarpRows / 32; ++i) {
+                const int c = 32 * h + chunk_step * i + lane, m = at.m * a.bn + c;
+                if (c < a.bn && m < a.M) x_next[i] = __ldg(a.xs + m);
+            }
             const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
             if (o < a.N) {
                 if (a.ws) w_next = __ldg(a.ws + o);
@@ -468,13 +472,14 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                 tc_fence_before_sync();
                 continue;
             }
-            float *xs_t = xs_s + (2 * b + ((n_local >> 1) & 1)) * kMaxBn;
-            if (et < kMaxBn) xs_t[et] = x_next;
+            __syncwarp();                    // the last tile's scales have been read
+#pragma unroll
+            for (int i = 0; i < kWarpRows / 32; ++i) xs_w[32 * i + lane] = x_next[i];
+            __syncwarp();
             const float ws = w_next, bo = b_next;
             const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
             const bool live = o < a.N;
             fetch(t + turn * step);
-            named_bar_sync(kEpiBar + set, groups * 128);
             ok = __all_sync(0xffffffffu,
                             mbar_wait(&acc_full[b], static_cast<uint32_t>(n_local / 2) & 1u, lim));
             if (!ok) break;
@@ -482,11 +487,12 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
             const uint32_t tb = tq + static_cast<uint32_t>(b * a.bn);
             YT *yo = Y + static_cast<size_t>(m0) * a.N + o;
             const bool whole = __all_sync(0xffffffffu, live);
-            const auto put = [&](uint32_t (&v)[kChunk], int c) {
-                finish_chunk<FMT>(v, smem_addr(xs_t + c), ws, bo, nf, Y);
+            const auto put = [&](uint32_t (&v)[kChunk], int c, uint32_t xs) {
+                finish_chunk<FMT>(v, xs, ws, bo, nf, Y);
                 store_chunk(v, yo + static_cast<size_t>(c) * a.N, a.N, mlim - c, live, whole);
             };
             int c = 2 * kChunk * h;
+            uint32_t xs = smem_addr(xs_w);
             do {
                 uint32_t v0[kChunk], v1[kChunk];
                 if (c < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(c), v0);
@@ -500,9 +506,10 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                         else mbar_arrive(&acc_empty[b]);
                     }
                 }
-                if (c < a.bn) put(v0, c);
-                if (c + kChunk < a.bn) put(v1, c + kChunk);
+                if (c < a.bn) put(v0, c, xs);
+                if (c + kChunk < a.bn) put(v1, c + kChunk, xs + 4 * kChunk);
                 c += chunk_step;
+                xs += 4 * 32;
             } while (c < a.bn);
         }
         if (__any_sync(0xffffffffu, (nf & 0x7FFF7FFFu) != 0) && lane == 0)
