@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "librtq.so")
 HEADER = os.path.join(ROOT, "include", "rtq.h")
 
 CU_SOURCES = ["api.cu", "simt.cu", "tc.cu", "xs.cu", "xp.cu", "ws.cu", "prep.cu", "pl.cu",
-              "noalloc.cu", "a8.cu", "a8q.cu", "a8v.cu", "a8api.cu"]
+              "noalloc.cu", "a8.cu", "a8q.cu", "a8q_f32.cu", "a8q_f16.cu",
+              "a8q_bf16.cu", "a8v.cu", "a8api.cu"]
 CPP_SOURCES = ["quantize.cpp", "st_loader.cpp"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -197,7 +197,7 @@ size_t pl_workspace_bytes(const PlInput *in, int count, int M);
 cudaError_t launch_pl_batch(const PlInput *in, int count, int M, void *ws, DevCtl *ctl,
                             cudaStream_t s);
 
-// Activations into 8 bits with one scale a row (a8q.cu), and the product of
+// Activations into 8 bits with one scale a row (a8q.cuh), and the product of
 // 8-bit activations with 8-bit weights (a8.cu).  Arguments are validated by
 // the caller (a8api.cu).  Rows of the row kernels stay in registers, which
 // bounds their length.
