@@ -415,39 +415,54 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     }
 }
 
-// Values of 8-bit rows: code * scale in fp32, rounded once to the type.
+// Values of 8-bit rows: code * scale in fp32, rounded once to the type.  A warp
+// takes kSpan vectors of one row at a time, all of its loads in flight at once.
+constexpr int kSpan = 4 * 32;
+
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
     a8_values_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales,
-                     T *__restrict__ out, int64_t vecs, int vk) {
+                     T *__restrict__ out, int M, int vecs) {
     constexpr int V = Vec<T>::n;
     pdl_wait_prior_grid();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < vecs;
-         i += step) {
-        const float s = __ldg(scales + i / vk);
-        uint32_t w[2];
-        if (V == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t *>(codes) + i);
-            w[1] = 0;
-        } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(codes) + i);
-            w[0] = u.x;
-            w[1] = u.y;
-        }
-        float f[V];
+    const int lane = threadIdx.x & 31;
+    const int spans = (vecs + kSpan - 1) / kSpan;
+    const int64_t total = static_cast<int64_t>(M) * spans;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+         u < total; u += step) {
+        const int64_t row = total <= INT32_MAX ? static_cast<int>(u) / spans : u / spans;
+        const int first = static_cast<int>(u - row * spans) * kSpan + lane;
+        const float s = __ldg(scales + row);
+        uint2 w[4];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint32_t b = (w[j >> 2] >> (8 * (j & 3))) & 0xFFu;
-            if (FMT == kFmtQ8) {
-                f[j] = static_cast<float>(static_cast<int8_t>(b)) * s;
-            } else {
-                const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b),
-                                                             __NV_E4M3);
-                f[j] = __half2float(__half(h)) * s;
+        for (int i = 0; i < 4; ++i) {
+            const int k = first + 32 * i;
+            w[i] = make_uint2(0u, 0u);
+            if (k < vecs) {
+                const int64_t at = row * vecs + k;
+                if (V == 4) w[i].x = __ldg(reinterpret_cast<const uint32_t *>(codes) + at);
+                else w[i] = __ldg(reinterpret_cast<const uint2 *>(codes) + at);
             }
         }
-        reinterpret_cast<uint4 *>(out)[i] = pack(f, out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = first + 32 * i;
+            if (k >= vecs) break;
+            float f[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const uint32_t b = ((j < 4 ? w[i].x : w[i].y) >> (8 * (j & 3))) & 0xFFu;
+                if (FMT == kFmtQ8) {
+                    f[j] = static_cast<float>(static_cast<int8_t>(b)) * s;
+                } else {
+                    const __half_raw h = __nv_cvt_fp8_to_halfraw(
+                        static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
+                    f[j] = __half2float(__half(h)) * s;
+                }
+            }
+            reinterpret_cast<uint4 *>(out)[row * vecs + k] = pack(f, out);
+        }
     }
 }
 
@@ -549,11 +564,11 @@ cudaError_t launch_rows_f(int fmt, const RowArgs &a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_values(int fmt, const uint8_t *codes, const float *scales, T *out, int M, int K,
                           cudaStream_t s) {
-    int64_t vecs = static_cast<int64_t>(M) * (K / Vec<T>::n);
-    int vk = K / Vec<T>::n;
-    void *args[] = {&codes, &scales, &out, &vecs, &vk};
-    const int64_t want = (vecs + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(want < 148 * 16 ? want : 148 * 16);
+    int vecs = K / Vec<T>::n;
+    void *args[] = {&codes, &scales, &out, &M, &vecs};
+    const int64_t warps = static_cast<int64_t>(M) * ((vecs + kSpan - 1) / kSpan);
+    const int64_t want = (warps + 7) / 8, most = 16 * static_cast<int64_t>(sm_count());
+    const unsigned grid = static_cast<unsigned>(want < most ? want : most);
     const void *fn = fmt == kFmtQ8 ? reinterpret_cast<const void *>(a8_values_kernel<T, kFmtQ8>)
                                    : reinterpret_cast<const void *>(a8_values_kernel<T, kFmtE4M3>);
     return launch_pdl(fn, grid, 256, args, s);
