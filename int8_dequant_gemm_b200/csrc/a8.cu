@@ -700,7 +700,7 @@ int sm_count() {
 // an SM takes in 128-byte rows of operands at one per 1.24 ns, which is slower
 // than the MMAs they feed; a tile's epilogue takes 0.47 + 0.0067 bn; a split adds
 // its cluster and the sum over distributed shared memory, a pair its
-// handshakes; in a walk of tiles the shorter of load and epilogue hides by 70 %.  Fitted to 1.7 thousand timings of M = 1 to 4096 against eight
+// handshakes; in a walk of tiles the shorter of load and epilogue hides by 70 %.  Fitted to 1.9 thousand timings of M = 1 to 4096 against eight
 // weight shapes from 512 x 512 to 8192 x 8192; over those shapes the plan taken
 // is on average 1.8 % slower than the best of them, at most 25 %.
 A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {

@@ -277,7 +277,7 @@ const char *rt_status_string(int status) {
     }
 }
 
-int rt_version(void) { return 200; }
+int rt_version(void) { return 210; }
 
 int rt_qgemm_auto_path(int fmt, int64_t M, int64_t N, int64_t K) {
     if (!rtq::fmt_valid(fmt) || M < 0 || N < 1 || K < 1) return -1;
