@@ -159,7 +159,8 @@ __device__ __forceinline__ void watch(uint32_t &nf, float v) {
 
 // A chunk of 16 activation rows of one weight row: y = acc * ws * xs + bias in
 // fp32 (fp32 results), or rounded and packed, rows 2i and 2i + 1 in word i
-// (16-bit results).  `xs`: the rows' scales in shared memory.
+// (16-bit results).  `xs`: the rows' scales in shared memory.  `nf` turns NaN once
+// one of the chunk's results, beyond the tensor's edge or not, is not finite.
 template <int FMT, typename YT>
 __device__ __forceinline__ void finish_chunk(uint32_t (&v)[kChunk], uint32_t xs, float ws, float bo,
                                              uint32_t &nf, const YT *type) {
@@ -194,11 +195,13 @@ __device__ __forceinline__ void finish_chunk(uint32_t (&v)[kChunk], uint32_t xs,
 // A finished chunk of one weight row: yo = this lane's output of its first row.
 // `whole`: every lane of the warp has an output.  16-bit results of an even N
 // go out as pairs: lanes 2i and 2i + 1 trade one value of two rows, and each
-// stores two neighbours of one row.
+// stores two neighbours of one row.  `seen`: finish_chunk's nf of this chunk; of a
+// chunk at the edge only the results that exist count toward nf.
 template <typename YT>
 __device__ __forceinline__ void store_chunk(const uint32_t (&v)[kChunk], YT *yo, int N, int rows,
-                                            bool live, bool whole) {
+                                            bool live, bool whole, uint32_t seen, uint32_t &nf) {
     const size_t ld = static_cast<size_t>(N);
+    if (whole && rows >= kChunk) nf |= seen;
     if constexpr (sizeof(YT) == 2) {
         if (whole && rows >= kChunk && (N & 1) == 0) {
             const int odd = threadIdx.x & 1;
@@ -220,8 +223,11 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[kChunk], YT *yo,
         } else if (live) {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i)
-                if (i < rows)
-                    yh[static_cast<size_t>(i) * ld] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+                if (i < rows) {
+                    const uint32_t one = (v[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+                    watch(nf, one, yo);
+                    yh[static_cast<size_t>(i) * ld] = static_cast<uint16_t>(one);
+                }
         }
     } else {
         float *yf = reinterpret_cast<float *>(yo);
@@ -231,7 +237,10 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[kChunk], YT *yo,
         } else if (live) {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i)
-                if (i < rows) yf[static_cast<size_t>(i) * ld] = __uint_as_float(v[i]);
+                if (i < rows) {
+                    watch(nf, __uint_as_float(v[i]));
+                    yf[static_cast<size_t>(i) * ld] = __uint_as_float(v[i]);
+                }
         }
     }
 }
@@ -488,8 +497,10 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
             YT *yo = Y + static_cast<size_t>(m0) * a.N + o;
             const bool whole = __all_sync(0xffffffffu, live);
             const auto put = [&](uint32_t (&v)[kChunk], int c, uint32_t xs) {
-                finish_chunk<FMT>(v, xs, ws, bo, nf, Y);
-                store_chunk(v, yo + static_cast<size_t>(c) * a.N, a.N, mlim - c, live, whole);
+                uint32_t seen = 0;
+                finish_chunk<FMT>(v, xs, ws, bo, seen, Y);
+                store_chunk(v, yo + static_cast<size_t>(c) * a.N, a.N, mlim - c, live, whole, seen,
+                            nf);
             };
             int c = 2 * kChunk * h;
             uint32_t xs = smem_addr(xs_w);
@@ -637,6 +648,9 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     }
     const int64_t share = (tiles * csize + grid - 1) / grid;   // tiles a CTA or cluster
     a.alt = share > 1;
+    // Clusters wait for their peers, so none of their CTAs may wait in tcgen05.alloc
+    // for another cluster's: pairs leave no registers beside them on an SM, and at
+    // most three CTAs of G = 1 fit, with 128 columns each at most.
     a.acc_cols = 32;
     while (a.acc_cols < (a.alt ? 2 : 1) * a.bn) a.acc_cols *= 2;
     a.stages = static_cast<int>(std::min<int64_t>(

@@ -370,6 +370,18 @@ def test_results_beyond_the_output_type_are_reported(rtq):
     assert rtq.device_status() == rtq.OK
 
 
+@pytest.mark.parametrize("M,N,K", [(80, 130, 512), (80, 130, 2048), (2500, 1000, 512), (5003, 1003, 1040), (3, 130, 512)])
+def test_only_results_that_exist_are_reported(rtq, M, N, K):
+    """A bias beyond fp16 that the sums bring back into range: what a tile computes
+    beyond the last row (0 + bias) is not an output."""
+    xc = torch.full((M, K), 100, dtype=torch.int8, device="cuda")
+    wc = torch.full((N, K), -100, dtype=torch.int8, device="cuda")
+    one = torch.ones(max(M, N), device="cuda")
+    b = torch.full((N,), 1e4 * K, device="cuda")
+    Y = rtq.qgemm_a8(Q8, xc, one[:M].contiguous(), wc, one[:N].contiguous(), bias=b, dtype=torch.float16)
+    assert bool((Y == 0).all()) and rtq.device_status() == rtq.OK
+
+
 def test_offsets_beyond_32_bits(rtq):
     """Y and X of more than 2^31 elements, checked on the first, middle and last rows."""
     M, N, K = 600_000, 4096, 32
