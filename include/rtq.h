@@ -570,7 +570,7 @@ rt_status rt_dequant_a8(int fmt, int dtype, const void *codes, const float *scal
  *   rt_qgemm_q8, or an e4m3 weight with row scales or, as rt_gemm_e4m3's,
  *   without (NULL); bias fp32 [N] or NULL; Y [M, N] of dtype.
  * The int8 sum is exact (int32) and is rounded to fp32 once; the e4m3 sum is
- * fp32.  Up to 8 rows run on the CUDA cores where that is faster, the rest on
+ * fp32.  A few rows run on the CUDA cores where that is faster, the rest on
  * tcgen05: one narrow tile a CTA, K split over clusters where there are few
  * tiles, persistent tiles otherwise, on CTA pairs where those are faster.
  * A row's int8 result does not depend on the call's other rows; an e4m3 row's
@@ -585,8 +585,8 @@ rt_status rt_qgemm_a8(int fmt, int dtype, const void *Xq, const float *x_scales,
  * activation rows and *split CTAs to a tile.  Returns -1 for what the product
  * refuses, else the sum of 1 where CTA pairs share an MMA over 256 weight rows
  * (otherwise 128 to a CTA) and 2 where a CTA takes one tile or one slice of its
- * K (otherwise CTAs walk the tiles); or 4: CUDA cores, 1 <= M <= 8, where that is
- * faster.  Without a device, the plan for 148 SMs. */
+ * K (otherwise CTAs walk the tiles); or 4: CUDA cores, 1 <= M <= 128, where that
+ * is faster.  Without a device, the plan for 148 SMs. */
 int rt_qgemm_a8_plan(int fmt, int64_t M, int64_t N, int64_t K, int *tile_rows, int *split);
 
 /*

@@ -756,18 +756,27 @@ A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
                   load + (per - 1.f) * (std::max(load, epi) + 0.3f * std::min(load, epi)) + epi +
                       (pair ? 0.9f : 0.f));
         }
-    // A few rows on the CUDA cores: 1.55 us less to set up; 0.08 us a 512-byte step
-    // of K, and a byte of weights costs its load or its arithmetic.  The tensor
-    // path takes weights from HBM at 5.4 TB/s at most.  Measured, us, CUDA cores
-    // and tensor cores: M = 1, int8, 512 x 512: 1.5 and 3.5, 512 x 2048 (K): 2.0 and
-    // 4.8, 8192 x 8192: 12.2 and 15.2; M = 8, 4096 x 4096: 9.1 and 6.2; e4m3, M = 1,
-    // 8192 x 8192: 17.1 and 15.6.
-    if (M >= 1 && M <= 8) {
+    // A few rows on the CUDA cores, 1 or 4 weight rows a warp (us less 2.75, which
+    // the tensor kernels take to set up): a 512-byte step of K costs a load's
+    // latency, a byte of weights its load or its arithmetic.  The tensor path takes
+    // weights from HBM at 5.4 TB/s at most.  Measured, us, CUDA cores and tensor
+    // cores: M = 1, int8, 512 x 512: 1.5 and 3.5, 512 x 2048 (K): 2.0 and 4.8, 8192 x
+    // 8192: 12.2 and 15.2; M = 8, 4096 x 4096: 6.6 and 6.2; M = 80, 512 x 512: 2.4 and
+    // 3.7, 2048 x 512: 5.5 and 3.7; e4m3, M = 1, 8192 x 8192: 17.1 and 15.6; M = 80,
+    // 512 x 512: 3.6 and 3.8.
+    if (M >= 1 && M <= 128) {
         const float mbytes = 1e-6f * static_cast<float>(N) * static_cast<float>(K);
-        const float byte_us = fmt == kFmtQ8 ? 0.12f + 0.031f * M : 0.14f + 0.089f * M;
+        const float steps = static_cast<float>(up(K, 512));
         least = std::max(least, mbytes / 5.4f);
-        offer({8, 1, 0, 0, K <= 512 && N >= 2048 ? 4 : 1},
-              0.08f * static_cast<float>(up(K, 512)) + byte_us * mbytes - 1.55f);
+        const bool q8 = fmt == kFmtQ8;
+        if (M <= 4 && !(K <= 512 && N >= 2048)) {
+            const float byte_us = q8 ? 0.12f + 0.031f * M : 0.14f + 0.089f * M;
+            offer({8, 1, 0, 0, 1}, -1.55f + 0.08f * steps + byte_us * mbytes);
+        } else {
+            const float work = mbytes * static_cast<float>(M <= 4 ? M : up(M, 8) * 8);
+            offer({8, 1, 0, 0, 4}, q8 ? -1.4f + 0.3f * (steps - 1.f) + (K <= 512 ? 0.045f : 0.03f) * work
+                                      : -1.15f + 0.7f * (steps - 1.f) + 0.085f * work);
+        }
     }
     return best;
 }

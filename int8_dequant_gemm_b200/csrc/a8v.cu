@@ -1,10 +1,10 @@
-// Product of a few 8-bit activation rows (M <= 8) with 8-bit weights on the CUDA
-// cores: at these sizes the weights' bytes are all there is, and a warp that
-// reads them straight into registers has neither the tensor path's set-up nor
-// its trip through shared memory and TMEM.
+// Product of a few 8-bit activation rows with 8-bit weights on the CUDA cores: at
+// these sizes the call is set-up and latency, and a warp that reads its operands
+// straight into registers has neither the tensor path's set-up nor its trip
+// through shared memory and TMEM.
 //
-// A warp takes RW weight rows and walks K in 512-byte steps, 16 bytes of every
-// row a lane; the MT activation rows come from L1.  int8: four-way integer dot
+// A warp takes RW weight rows and MT activation rows and walks K in 512-byte
+// steps, 16 bytes of every row a lane; the activation rows come from L1.  int8: four-way integer dot
 // products, exact in int32.  e4m3: exact products, fp32 sums.  The RW * MT sums
 // are added over the lanes by halving (each step trades half of the values for
 // the other half), so a value ends in 32 / (RW MT) lanes of its own; the order of
@@ -62,11 +62,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int lane = threadIdx.x & 31;
     const int64_t o0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * RW;
     if (o0 >= N) return;
+    const int m0 = static_cast<int>(blockIdx.y) * MT;
     const uint8_t *w[RW], *x[MT];
 #pragma unroll
     for (int r = 0; r < RW; ++r) w[r] = Wq + min(o0 + r, static_cast<int64_t>(N) - 1) * K;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = Xq + static_cast<int64_t>(min(m, M - 1)) * K;
+    for (int m = 0; m < MT; ++m) x[m] = Xq + static_cast<int64_t>(min(m0 + m, M - 1)) * K;
     Acc acc[kVals] = {};
     constexpr int kSteps = RW > 2 ? 2 : 4;   // 512-byte steps with loads in flight at once
     for (int k0 = lane * 16; k0 < K; k0 += kSteps * 512) {
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int e = 32 / kVals / 2; e >= 1; e /= 2) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], e);
     // lane group lane / (32 / kVals) holds value m * RW + r
-    const int v = lane / (32 / kVals), m = v / RW;
+    const int v = lane / (32 / kVals), m = m0 + v / RW;
     const int64_t o = o0 + v % RW;
     float out = 0.f;
     if (lane % (32 / kVals) == 0 && m < M && o < N) {
@@ -148,7 +149,8 @@ cudaError_t launch_few(const void *Xq, const float *xs, const void *Wq, const fl
     void *args[] = {&x, &xs, &w, &wsc, &bias, &y, &M, &N, &K, &ctl};
     cudaLaunchConfig_t cfg = {};
     const int64_t rows = static_cast<int64_t>(RW) * kWarps;
-    cfg.gridDim = dim3(static_cast<unsigned>((N + rows - 1) / rows), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((N + rows - 1) / rows),
+                       static_cast<unsigned>((M + MT - 1) / MT), 1);
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

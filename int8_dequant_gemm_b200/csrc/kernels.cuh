@@ -226,8 +226,8 @@ cudaError_t launch_qgemm_a8(const A8Plan &plan, int fmt, int dtype, const void *
                             const void *Wq, const float *wsc, const float *bias, void *Y, int M,
                             int N, int K, DevCtl *ctl, cudaStream_t s);
 
-// The same product for M <= 8 on the CUDA cores, rw = 1 or 4 weight rows a warp
-// (a8v.cu).
+// The same product on the CUDA cores, for few activation rows: rw = 1 or 4 weight
+// rows and up to 8 activation rows a warp (a8v.cu).
 cudaError_t launch_qgemm_a8_few(int rw, int fmt, int dtype, const void *Xq, const float *xs,
                                 const void *Wq, const float *wsc, const float *bias, void *Y, int M,
                                 int N, int K, DevCtl *ctl, cudaStream_t s);

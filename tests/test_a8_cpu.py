@@ -99,14 +99,14 @@ def test_product_plan():
     assert rtq.a8_plan(-1, 24, 64) is None and rtq.a8_plan(4, 24, 131072) is None
     assert rtq.a8_plan(4, 24, 64, Q4) is None
     for fmt in (Q8, E4M3):
-        assert rtq.a8_plan(1, 512, 512, fmt)["cores"] and not rtq.a8_plan(9, 512, 512, fmt)["cores"]
+        assert rtq.a8_plan(1, 512, 512, fmt)["cores"] and not rtq.a8_plan(129, 64, 64, fmt)["cores"]
         assert not rtq.a8_plan(8, 8192, 8192, fmt)["cores"]
         for M in (0, 1, 8, 16, 17, 80, 128, 129, 300, 4096, 65536, 2 ** 31 - 1024):
             for N in (1, 128, 512, 4096):
                 for K in (16, 512, 2048, 131056):
                     p = rtq.a8_plan(M, N, K, fmt)
                     if p["cores"]:
-                        assert 1 <= M <= 8
+                        assert 1 <= M <= 128
                         continue
                     assert 1 <= p["split"] <= min(8, -(-K // 128))
                     assert p["rows"] % (32 if p["pair"] else 16) == 0 and 16 <= p["rows"] <= 256

@@ -494,7 +494,7 @@ def test_explicit_stream_and_one_buffer_reused(rtq):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M,N,K", [(80, 512, 2048), (100, 30000, 128), (2500, 1000, 512), (5003, 1003, 1040)])
+@pytest.mark.parametrize("M,N,K", [(128, 129, 4112), (100, 30000, 128), (2500, 1000, 512), (5003, 1003, 1040)])
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
 def test_injected_missing_box_times_out_and_recovers(rtq, M, N, K, fmt):
     xc, xs, wc, ws, b = operands(fmt, M, N, K, seed=13)
