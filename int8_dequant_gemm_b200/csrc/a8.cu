@@ -327,74 +327,75 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     pdl_launch_dependents();
     bool ok = true;
 
+    // The TMA and MMA warps run their loops whole and in uniform control flow -- a
+    // wait that gives up clears `good`, which skips later waits and issues but
+    // no loop -- so that counters and descriptors stay in uniform registers.  With
+    // loops left early, or run by one lane, a stage took 300 ns to issue.
     if (warp == 0) {
         // ============================================================ TMA
         // (Test hook: with `inject` the first weight box is never requested.)
-        if (lane == 0) {
-            int s = 0, j = 0;
-            uint32_t par = 1;
-            for (int t = first; t < n_tiles && ok; t += step) {
-                const TileAt at(t, a.n_m, a.n_o);
-                const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
-                const int my = at.m * a.bn + (PAIR ? rank * (a.bn / 2) : 0);
-                for (int kb = kb0; kb < kb1; ++kb, ++j) {
-                    if (j >= a.stages && !mbar_wait(&empty[s], par, lim)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool skip = j == 0 && leader && ctl->inject;
-                    const uint32_t dst = base + static_cast<uint32_t>(s * sbytes);
+        const bool inject = leader && ctl->inject;
+        bool good = true;
+        int s = 0, j = 0;
+        uint32_t par = 1;
+        for (int t = first; t < n_tiles; t += step) {
+            const TileAt at(t, a.n_m, a.n_o);
+            const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
+            const int my = at.m * a.bn + (PAIR ? rank * (a.bn / 2) : 0);
+            for (int kb = kb0; kb < kb1; ++kb, ++j) {
+                if (good && j >= a.stages) good = mbar_wait(&empty[s], par, lim);
+                const uint32_t dst = base + static_cast<uint32_t>(s * sbytes);
+                const uint32_t bar = smem_addr(&full[s]);
+                if (elect_one() && good) {
                     if (PAIR) {
-                        const uint32_t cbar = cluster_map(smem_addr(&full[s]), 0);
+                        const uint32_t cbar = cluster_map(bar, 0);
                         if (leader) mbar_expect_tx(&full[s], 2u * static_cast<uint32_t>(sbytes));
-                        if (!skip) tma_load_2d_pair(dst, &w_map, kb * kKBytes, oy, cbar);
+                        if (j > 0 || !inject) tma_load_2d_pair(dst, &w_map, kb * kKBytes, oy, cbar);
                         tma_load_2d_pair(dst + kABytes, &x_map, kb * kKBytes, my, cbar);
                     } else {
                         mbar_expect_tx(&full[s], static_cast<uint32_t>(sbytes));
-                        if (!skip) tma_load_2d(dst, &w_map, kb * kKBytes, oy, &full[s]);
+                        if (j > 0 || !inject) tma_load_2d(dst, &w_map, kb * kKBytes, oy, &full[s]);
                         tma_load_2d(dst + kABytes, &x_map, kb * kKBytes, my, &full[s]);
                     }
-                    if (++s == a.stages) {
-                        s = 0;
-                        par ^= 1;
-                    }
                 }
-            }
-            // Before the CTA may exit, every box it requested has landed
-            // (immediate unless a consumer gave up; a pair's boxes are counted
-            // by its even CTA, which the odd one meets before it exits).
-            if (leader) {
-                for (int i = 0; i < a.stages && i < j; ++i) {
-                    const int last_j = i + ((j - 1 - i) / a.stages) * a.stages;
-                    if (!(last_j == 0 && ctl->inject))
-                        mbar_wait(&full[i], static_cast<uint32_t>(last_j / a.stages) & 1u, lim);
+                if (++s == a.stages) {
+                    s = 0;
+                    par ^= 1;
                 }
             }
         }
-        __syncwarp();
+        // Before the CTA may exit, every box it requested has landed (immediate
+        // unless a consumer gave up; a pair's boxes are counted by its even CTA,
+        // which the odd one meets before it exits).  A box that was not
+        // requested after a failure makes its wait run out.
+        if (leader) {
+            for (int i = 0; i < a.stages && i < j; ++i) {
+                const int last_j = i + ((j - 1 - i) / a.stages) * a.stages;
+                if (good && !(last_j == 0 && inject))
+                    mbar_wait(&full[i], static_cast<uint32_t>(last_j / a.stages) & 1u, lim);
+            }
+        }
+        ok = good;
     } else if (warp == 1) {
         // ============================================================ MMA issue
         if (leader) {
             const uint32_t idesc = idesc_8bit(FMT, (PAIR ? 2 : 1) * kTileRows, a.bn);
+            bool good = true;
             int s = 0, n_local = 0;
             uint32_t par = 0;
-            for (int t = first; t < n_tiles && ok; t += step, ++n_local) {
+            for (int t = first; t < n_tiles; t += step, ++n_local) {
                 const int b = n_local & 1;
-                if (n_local >= 2)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&acc_empty[b],
-                                              static_cast<uint32_t>((n_local / 2) - 1) & 1u, lim));
-                if (!ok) break;
-                tc_fence_after_sync();
+                if (good && n_local >= 2)
+                    good = mbar_wait(&acc_empty[b], static_cast<uint32_t>((n_local / 2) - 1) & 1u,
+                                     lim);
                 const uint32_t d = tmem + static_cast<uint32_t>(b * a.bn);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&full[s], par, lim));
-                    if (!ok) break;
+                    if (good) good = mbar_wait(&full[s], par, lim);
                     tc_fence_after_sync();
                     const uint32_t st = base + static_cast<uint32_t>(s * sbytes);
                     const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
                     const int left = a.K - kb * kKBytes;       // 32 K a step; rest is zero fill
-                    if (elect_one()) {
+                    if (elect_one() && good) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             if (kk * 32 < left)
@@ -403,19 +404,17 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                         if (PAIR) tc_commit_pair_mc(&empty[s], kBoth);
                         else tc_commit(&empty[s]);
                     }
-                    __syncwarp();
                     if (++s == a.stages) {
                         s = 0;
                         par ^= 1;
                     }
                 }
-                if (!ok) break;
-                if (elect_one()) {
+                if (elect_one() && good) {
                     if (PAIR) tc_commit_pair_mc(&acc_full[b], kBoth);
                     else tc_commit(&acc_full[b]);
                 }
-                __syncwarp();
             }
+            ok = __all_sync(0xffffffffu, good);
             if (!ok) {                       // issued MMAs end before the CTA does
                 if (elect_one()) {
                     if (PAIR) tc_commit_pair_mc(drain, 1);
