@@ -41,8 +41,13 @@
 namespace rtq {
 namespace {
 
-constexpr int kKBytes = 128;                       // K per stage: one swizzled row
-constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights a stage
+constexpr int kKBytes = 128;                       // K of an atom: one swizzled row
+constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights an atom
+// Atoms a stage: issuing a stage costs about 330 cycles beside its MMAs' 25 each,
+// which one atom of a pair's 256-wide MMAs (128 cycles each) covers; narrower
+// tiles take two at a time (80 x 512 x 2048 e4m3 5.0 -> 4.6 us, 512 x 4096 x 4096
+// 12.3 -> 10.4; 8192^3 on pairs 369 -> 381).
+constexpr int stage_atoms(int pair) { return pair ? 1 : 2; }
 // Epilogue groups G of four warps, one per TMEM lane quadrant: 4 for persistent
 // tiles, 1 where a CTA has one narrow tile (192 threads and at most half an
 // SM's registers and shared memory, so the next kernel's CTA starts beside it).
@@ -66,8 +71,11 @@ struct A8Args {
                              // scales [16][kWarpRows], barriers and words
 };
 
-__host__ __device__ constexpr int stage_bytes(int bn, int pair) {
+__host__ __device__ constexpr int atom_bytes(int bn, int pair) {
     return kABytes + (pair ? bn / 2 : bn) * kKBytes;
+}
+__host__ __device__ constexpr int stage_bytes(int bn, int pair) {
+    return stage_atoms(pair) * atom_bytes(bn, pair);
 }
 
 // The ring; a split's partial sums reuse it.
@@ -263,7 +271,7 @@ template <int FMT, typename YT, bool PAIR, int G>
 __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     a8_qgemm_kernel(const __grid_constant__ CUtensorMap w_map,
                     const __grid_constant__ CUtensorMap x_map, const A8Args a, DevCtl *ctl) {
-    constexpr int kEpiWarp0 = epi_warp0(G), kEpiWarps = 4 * G;
+    constexpr int kEpiWarp0 = epi_warp0(G), kEpiWarps = 4 * G, kAtoms = stage_atoms(PAIR);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -286,8 +294,9 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     const int n_tiles = a.n_o * a.n_m;
     const int first = static_cast<int>(blockIdx.x) / csize;
     const int step = static_cast<int>(gridDim.x) / csize;
-    const int sbytes = stage_bytes(a.bn, PAIR);
+    const int abytes = atom_bytes(a.bn, PAIR), sbytes = kAtoms * abytes;
     const unsigned long long *lim = &ctl->wait_ns;
+    const bool inject = leader && ctl->inject;     // read before the wait below
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -334,7 +343,6 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     if (warp == 0) {
         // ============================================================ TMA
         // (Test hook: with `inject` the first weight box is never requested.)
-        const bool inject = leader && ctl->inject;
         bool good = true;
         int s = 0, j = 0;
         uint32_t par = 1;
@@ -342,20 +350,26 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
             const TileAt at(t, a.n_m, a.n_o);
             const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
             const int my = at.m * a.bn + (PAIR ? rank * (a.bn / 2) : 0);
-            for (int kb = kb0; kb < kb1; ++kb, ++j) {
+            for (int kb = kb0; kb < kb1; kb += kAtoms, ++j) {
                 if (good && j >= a.stages) good = mbar_wait(&empty[s], par, lim);
-                const uint32_t dst = base + static_cast<uint32_t>(s * sbytes);
-                const uint32_t bar = smem_addr(&full[s]);
+                const int atoms = min(kAtoms, kb1 - kb);
+                const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * atoms * abytes);
                 if (elect_one() && good) {
-                    if (PAIR) {
-                        const uint32_t cbar = cluster_map(bar, 0);
-                        if (leader) mbar_expect_tx(&full[s], 2u * static_cast<uint32_t>(sbytes));
-                        if (j > 0 || !inject) tma_load_2d_pair(dst, &w_map, kb * kKBytes, oy, cbar);
-                        tma_load_2d_pair(dst + kABytes, &x_map, kb * kKBytes, my, cbar);
-                    } else {
-                        mbar_expect_tx(&full[s], static_cast<uint32_t>(sbytes));
-                        if (j > 0 || !inject) tma_load_2d(dst, &w_map, kb * kKBytes, oy, &full[s]);
-                        tma_load_2d(dst + kABytes, &x_map, kb * kKBytes, my, &full[s]);
+                    const uint32_t cbar = PAIR ? cluster_map(smem_addr(&full[s]), 0) : 0;
+                    if (leader) mbar_expect_tx(&full[s], bytes);
+#pragma unroll
+                    for (int u = 0; u < kAtoms; ++u) {
+                        if (u == atoms) break;
+                        const uint32_t dst = base + static_cast<uint32_t>(s * sbytes + u * abytes);
+                        const int x = (kb + u) * kKBytes;
+                        const bool skip = inject && j == 0 && u == 0;
+                        if (PAIR) {
+                            if (!skip) tma_load_2d_pair(dst, &w_map, x, oy, cbar);
+                            tma_load_2d_pair(dst + kABytes, &x_map, x, my, cbar);
+                        } else {
+                            if (!skip) tma_load_2d(dst, &w_map, x, oy, &full[s]);
+                            tma_load_2d(dst + kABytes, &x_map, x, my, &full[s]);
+                        }
                     }
                 }
                 if (++s == a.stages) {
@@ -389,17 +403,20 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                     good = mbar_wait(&acc_empty[b], static_cast<uint32_t>((n_local / 2) - 1) & 1u,
                                      lim);
                 const uint32_t d = tmem + static_cast<uint32_t>(b * a.bn);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += kAtoms) {
                     if (good) good = mbar_wait(&full[s], par, lim);
                     tc_fence_after_sync();
                     const uint32_t st = base + static_cast<uint32_t>(s * sbytes);
                     const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
-                    const int left = a.K - kb * kKBytes;       // 32 K a step; rest is zero fill
+                    const uint64_t next = static_cast<uint64_t>(abytes >> 4);
+                    // K left in this CTA's slice; the rest of the last atom is zero fill
+                    const int left = min(a.K, kb1 * kKBytes) - kb * kKBytes;
                     if (elect_one() && good) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
+                        for (int kk = 0; kk < 4 * kAtoms; ++kk)        // 32 K each
                             if (kk * 32 < left)
-                                mma_8bit<FMT, PAIR>(d, ad + 2 * kk, bd + 2 * kk, idesc,
+                                mma_8bit<FMT, PAIR>(d, ad + (kk >> 2) * next + 2 * (kk & 3),
+                                                    bd + (kk >> 2) * next + 2 * (kk & 3), idesc,
                                                     (kb > kb0 || kk > 0) ? 1u : 0u);
                         if (PAIR) tc_commit_pair_mc(&empty[s], kBoth);
                         else tc_commit(&empty[s]);
@@ -654,7 +671,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     while (a.acc_cols < (a.alt ? 2 : 1) * a.bn) a.acc_cols *= 2;
     a.stages = static_cast<int>(std::min<int64_t>(
         std::min(kMaxStages, (G == 1 ? kSmemSmall : kSmemMax) / stage_bytes(a.bn, PAIR)),
-        share * ((nkb + a.split - 1) / a.split)));
+        share * ((((nkb + a.split - 1) / a.split) + stage_atoms(PAIR) - 1) / stage_atoms(PAIR))));
     a.tail_off = ring_bytes(a, PAIR);
     cfg.dynamicSmemBytes = a.tail_off + kTailBytes + 1024;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
