@@ -67,8 +67,10 @@ struct A8Args {
     int n_o, n_m;            // weight tiles, activation tiles
     int acc_cols;
     int alt;                 // two epilogue sets take turns
-    int tail_off;            // after the ring: each epilogue warp's activation
-                             // scales [16][kWarpRows], barriers and words
+    int red_off;             // after the ring, split: partial sums of this rank's columns,
+                             // [rank][column][128]
+    int tail_off;            // after both: each epilogue warp's activation
+                             // scales [4 G][2][kWarpWords], barriers and words
 };
 
 __host__ __device__ constexpr int atom_bytes(int bn, int pair) {
@@ -78,14 +80,10 @@ __host__ __device__ constexpr int stage_bytes(int bn, int pair) {
     return stage_atoms(pair) * atom_bytes(bn, pair);
 }
 
-// The ring; a split's partial sums reuse it.
-__host__ inline int ring_bytes(const A8Args &a, int pair) {
-    const int ring = a.stages * stage_bytes(a.bn, pair);
-    const int red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
-    return ring > red ? ring : red;
-}
 constexpr int kWarpRows = 128;                     // activation rows of a tile an epilogue warp takes
-constexpr int kTailBytes = 16 * kWarpRows * 4 + (2 * kMaxStages + 5) * 8 + 16;
+constexpr int kWarpWords = kWarpRows + 64;         // their scales, then each lane's ws and bias
+constexpr int scale_bytes(int G) { return 4 * G * 2 * kWarpWords * 4; }
+constexpr int tail_bytes(int G) { return scale_bytes(G) + (2 * kMaxStages + 5) * 8 + 16; }
 
 // Instruction descriptors (A and B K-major): accumulator s32 (2) or f32 (1),
 // operand type 1 = s8 of kind::i8, 0 = e4m3 of kind::f8f6f4.
@@ -267,7 +265,7 @@ struct TileAt {
     }
 };
 
-template <int FMT, typename YT, bool PAIR, int G>
+template <int FMT, typename YT, bool PAIR, int G, bool SPLIT>
 __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     a8_qgemm_kernel(const __grid_constant__ CUtensorMap w_map,
                     const __grid_constant__ CUtensorMap x_map, const A8Args a, DevCtl *ctl) {
@@ -278,19 +276,19 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     const uint32_t base = smem_addr(smem);
     uint8_t *tail = smem + a.tail_off;
     float *xs_s = reinterpret_cast<float *>(tail);
-    uint64_t *full = reinterpret_cast<uint64_t *>(tail + 16 * kWarpRows * 4);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + scale_bytes(G));
     uint64_t *empty = full + kMaxStages;
     uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile uint32_t *failed = tmem_slot + 1;     // split: this rank has no sum
+    volatile uint32_t *failed = tmem_slot + 1;     // split: a rank has no sum
 
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-    const int split = PAIR ? 1 : a.split;
+    const int split = SPLIT ? a.split : 1;
     const int csize = PAIR ? 2 : split;
     const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const bool leader = !PAIR || rank == 0;
     const int nkb = (a.K + kKBytes - 1) / kKBytes;
-    const int kb0 = nkb * (PAIR ? 0 : rank) / split, kb1 = nkb * ((PAIR ? 0 : rank) + 1) / split;
+    const int kb0 = SPLIT ? nkb * rank / split : 0, kb1 = SPLIT ? nkb * (rank + 1) / split : nkb;
     const int n_tiles = a.n_o * a.n_m;
     const int first = static_cast<int>(blockIdx.x) / csize;
     const int step = static_cast<int>(gridDim.x) / csize;
@@ -327,6 +325,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     tc_fence_before_sync();
     __syncthreads();
     if (PAIR) cluster_sync();      // the peer's barriers are initialised
+    else if (SPLIT) cluster_arrive();      // this rank takes its peers' sums
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     // Every operand, the weights and scales too, may be the previous kernel's
@@ -335,6 +334,16 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     bool ok = true;
+    float wsc[4] = {1.f, 1.f, 1.f, 1.f}, bo[4] = {};       // of the split-K sum's weight rows
+    if (SPLIT && warp >= kEpiWarp0) {
+        const TileAt at(first, a.n_m, a.n_o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = at.o * kTileRows + 4 * lane + i;
+            if (n < a.N && a.ws) wsc[i] = __ldg(a.ws + n);
+            if (n < a.N && a.bias) bo[i] = __ldg(a.bias + n);
+        }
+    }
 
     // The TMA and MMA warps run their loops whole and in uniform control flow -- a
     // wait that gives up clears `good`, which skips later waits and issues but
@@ -454,57 +463,69 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
         YT *const Y = static_cast<YT *>(a.Y);
         uint32_t nf = 0;                     // NaN once an output is not finite
-        // The next tile's scales and bias are loaded while this one is stored.  Each
-        // warp keeps the scales of its own activation rows: the warps share no
-        // barrier, which a warp whose wait gave up would not come to.
-        float *const xs_w = xs_s + ew * kWarpRows;
-        float x_next[kWarpRows / 32] = {}, w_next = 1.f, b_next = 0.f;
-        auto fetch = [&](int t) {
-            if (split > 1 || t >= n_tiles) return;
+        // The next tile's scales and bias are copied while this one is stored, past
+        // the registers, of which the arithmetic needs all.  Each warp keeps the scales
+        // of its own activation rows: the warps share no barrier, which a warp whose
+        // wait gave up would not come to.
+        uint32_t xs_w = smem_addr(xs_s) + ew * (2 * kWarpWords * 4), flip = 0;
+        auto fetch = [&](int t, uint32_t to) {
+            if (SPLIT || t >= n_tiles) return;
             const TileAt at(t, a.n_m, a.n_o);
 #pragma unroll
             for (int i = 0; i < kWarpRows / 32; ++i) {
                 const int c = 32 * h + chunk_step * i + lane, m = at.m * a.bn + c;
-                if (c < a.bn && m < a.M) x_next[i] = __ldg(a.xs + m);
+                const bool there = c < a.bn && m < a.M;
+                cp_async_word(to + 4 * (32 * i + lane), a.xs + (there ? m : 0), there);
             }
             const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
-            if (o < a.N) {
-                if (a.ws) w_next = __ldg(a.ws + o);
-                if (a.bias) b_next = __ldg(a.bias + o);
-            }
+            const bool there = o < a.N;
+            const uint32_t own = to + 4 * (kWarpRows + lane);
+            if (a.ws) cp_async_word(own, a.ws + (there ? o : 0), there);
+            else sts_u32(own, __float_as_uint(1.f));
+            if (a.bias) cp_async_word(own + 128, a.bias + (there ? o : 0), there);
+            else sts_u32(own + 128, 0);
         };
-        fetch(first + set * step);
+        fetch(first + set * step, xs_w);
+        if (SPLIT) cluster_wait();      // the peers have started
         int n_local = set;
         for (int t = first + set * step; t < n_tiles && ok; t += turn * step, n_local += turn) {
             const TileAt at(t, a.n_m, a.n_o);
             const int b = n_local & 1;
             const int m0 = at.m * a.bn;
             const int mlim = min(a.bn, a.M - m0);
-            if (split > 1) {
-                // partial sums into this CTA's shared memory, [column][lane]
+            if (SPLIT) {
+                // each rank's columns of this partial sum into its shared memory
                 ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[0], 0, lim));
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t *red = reinterpret_cast<uint32_t *>(smem);
-                for (int c = kChunk * h; c < a.bn; c += kChunk * G) {
-                    uint32_t v[16];
+                const uint32_t own = static_cast<uint32_t>(a.bn / split);
+                const uint32_t to = base + static_cast<uint32_t>(a.red_off) +
+                                    (rank * own * kTileRows + q * 32 + lane) * 4;
+                uint32_t peer = 0, at_p = 0;
+                for (int c = 0; c < a.bn; c += kChunk) {
+                    uint32_t v[kChunk];
                     tmem_ld_x16(tq + static_cast<uint32_t>(c), v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        red[(c + i) * kTileRows + q * 32 + lane] = v[i];
+                    for (int i = 0; i < kChunk; ++i) {
+                        st_cluster_u32(cluster_map(to + at_p * kTileRows * 4, peer), v[i]);
+                        if (++at_p == own) {
+                            at_p = 0;
+                            ++peer;
+                        }
+                    }
                 }
-                tc_fence_before_sync();
-                continue;
+                break;
             }
-            __syncwarp();                    // the last tile's scales have been read
-#pragma unroll
-            for (int i = 0; i < kWarpRows / 32; ++i) xs_w[32 * i + lane] = x_next[i];
-            __syncwarp();
-            const float ws = w_next, bo = b_next;
+            const uint32_t mine = xs_w + flip;
+            flip ^= kWarpWords * 4;
+            cp_async_wait_all();
+            __syncwarp();                    // and the tile before's have been read
+            const float ws = __uint_as_float(lds_u32(mine + 4 * (kWarpRows + lane)));
+            const float bo = __uint_as_float(lds_u32(mine + 4 * (kWarpRows + 32 + lane)));
             const int o = (PAIR ? 2 * at.o + rank : at.o) * kTileRows + q * 32 + lane;
             const bool live = o < a.N;
-            fetch(t + turn * step);
+            fetch(t + turn * step, xs_w + flip);
             ok = __all_sync(0xffffffffu,
                             mbar_wait(&acc_full[b], static_cast<uint32_t>(n_local / 2) & 1u, lim));
             if (!ok) break;
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                             nf);
             };
             int c = 2 * kChunk * h;
-            uint32_t xs = smem_addr(xs_w);
+            uint32_t xs = mine;
             do {
                 uint32_t v0[kChunk], v1[kChunk];
                 if (c < a.bn) tmem_ld_x16(tb + static_cast<uint32_t>(c), v0);
@@ -539,72 +560,66 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                 xs += 4 * 32;
             } while (c < a.bn);
         }
+        cp_async_wait_all();                 // after a wait that gave up
         if (__any_sync(0xffffffffu, (nf & 0x7FFF7FFFu) != 0) && lane == 0)
             atomicOr(&ctl->status, 1u << kStatusRange);
     }
+    if (SPLIT && warp < kEpiWarp0) {
+        __syncwarp();
+        cluster_wait();
+    }
     if (!ok) {
         atomicOr(&ctl->status, 1u << kStatusTimeout);
-        *failed = 1;
+        if (SPLIT)
+            for (int r = 0; r < split; ++r)
+                st_cluster_u32(cluster_map(smem_addr(const_cast<uint32_t *>(failed)),
+                                           static_cast<uint32_t>(r)), 1);
     }
     tc_fence_before_sync();
-    if (csize > 1) cluster_sync();
+    if (PAIR || SPLIT) cluster_sync();
     else __syncthreads();
-    if (!PAIR && split > 1) {
+    if (SPLIT && warp >= kEpiWarp0 && *failed == 0) {
         // ============================================================ split-K sum
-        // Rank r of the cluster adds and stores columns [bn r / split,
-        // bn (r + 1) / split) of all ranks' partial sums, in rank order.
-        bool all = true;
-        for (int r = 0; r < split; ++r)
-            all = all && ld_cluster_u32(cluster_map(smem_addr(const_cast<uint32_t *>(failed)),
-                                                    static_cast<uint32_t>(r))) == 0;
-        if (warp >= kEpiWarp0 && all) {
-            const TileAt at(first, a.n_m, a.n_o);
-            YT *const Y = static_cast<YT *>(a.Y);
-            float nf = 0.f;
-            const int m0 = at.m * a.bn;
-            const int c1 = min(a.bn * (rank + 1) / split, a.M - m0);
-            const int o = at.o * kTileRows + 4 * lane;
-            float wsc[4], bo[4];
+        // Each rank has sent its peers their columns, a store a column and warp, and
+        // one cluster barrier orders them (80 x 512 x 2048 e4m3: 3.7 us; with the sums
+        // read from the peers, between two barriers, 4.6).  Rank r of the cluster adds and stores columns [bn r / split,
+        // bn (r + 1) / split): all ranks' partial sums of them, in rank order.
+        const TileAt at(first, a.n_m, a.n_o);
+        YT *const Y = static_cast<YT *>(a.Y);
+        float nf = 0.f;
+        const int own = a.bn / split, m0 = at.m * a.bn + rank * own;
+        const int c1 = min(own, a.M - m0);
+        const int o = at.o * kTileRows + 4 * lane;
+        for (int c = warp - kEpiWarp0; c < c1; c += kEpiWarps) {
+            const float xv = __ldg(a.xs + m0 + c);
+            const float *part =
+                reinterpret_cast<const float *>(smem + a.red_off) + c * kTileRows + 4 * lane;
+            float sf[4] = {0.f, 0.f, 0.f, 0.f};
+            int si[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                wsc[i] = o + i < a.N && a.ws ? __ldg(a.ws + o + i) : 1.f;
-                bo[i] = o + i < a.N && a.bias ? __ldg(a.bias + o + i) : 0.f;
-            }
-            for (int c = a.bn * rank / split + warp - kEpiWarp0; c < c1; c += kEpiWarps) {
-                const float xv = __ldg(a.xs + m0 + c);
-                const uint32_t at_c = base + static_cast<uint32_t>((c * kTileRows + 4 * lane) * 4);
-                float4 p[8];
+            for (int r = 0; r < 8; ++r)
+                if (r < split) {
+                    const float4 p = *reinterpret_cast<const float4 *>(part + r * own * kTileRows);
+                    const float e[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < split) p[r] = ld_cluster_f4(cluster_map(at_c, static_cast<uint32_t>(r)));
-                float sf[4] = {0.f, 0.f, 0.f, 0.f};
-                int si[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < split) {
-                        const float e[4] = {p[r].x, p[r].y, p[r].z, p[r].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (FMT == kFmtQ8) si[i] += __float_as_int(e[i]);
-                            else sf[i] += e[i];
-                        }
-                    }
-                YT *yo = Y + static_cast<size_t>(m0 + c) * a.N + o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (o + i < a.N) {
-                        const float s = FMT == kFmtQ8 ? __int2float_rn(si[i]) : sf[i];
-                        const YT y = to_type(fmaf(s * wsc[i], xv, bo[i]), Y);
-                        nf = fmaf(to_f32(y), 0.f, nf);
-                        yo[i] = y;
+                    for (int i = 0; i < 4; ++i) {
+                        if (FMT == kFmtQ8) si[i] += __float_as_int(e[i]);
+                        else sf[i] += e[i];
                     }
                 }
+            YT *yo = Y + static_cast<size_t>(m0 + c) * a.N + o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (o + i < a.N) {
+                    const float s = FMT == kFmtQ8 ? __int2float_rn(si[i]) : sf[i];
+                    const YT y = to_type(fmaf(s * wsc[i], xv, bo[i]), Y);
+                    nf = fmaf(to_f32(y), 0.f, nf);
+                    yo[i] = y;
+                }
             }
-            if (__any_sync(0xffffffffu, nf != 0.f) && lane == 0)
-                atomicOr(&ctl->status, 1u << kStatusRange);
         }
-        __syncwarp();
-        cluster_sync();                      // no rank exits while another reads its sums
+        if (__any_sync(0xffffffffu, nf != 0.f) && lane == 0)
+            atomicOr(&ctl->status, 1u << kStatusRange);
     }
     if (warp == 1) {
         tc_fence_after_sync();
@@ -613,7 +628,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     }
 }
 
-template <int FMT, typename YT, bool PAIR, int G>
+template <int FMT, typename YT, bool PAIR, int G, bool SPLIT>
 cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const void *Wq,
                       const float *wsc, const float *bias, void *Y, int M, int N, int K,
                       DevCtl *ctl, cudaStream_t st) {
@@ -622,9 +637,8 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if ((e = smem_attr_once(a8_qgemm_kernel<FMT, YT, PAIR, G>, 227 * 1024, dev, attr_done)) !=
-        cudaSuccess)
-        return e;
+    const auto kernel = a8_qgemm_kernel<FMT, YT, PAIR, G, SPLIT>;
+    if ((e = smem_attr_once(kernel, 227 * 1024, dev, attr_done)) != cudaSuccess) return e;
     A8Args a = {};
     a.xs = xs;
     a.ws = wsc;
@@ -634,7 +648,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     a.N = N;
     a.K = K;
     a.bn = plan.bn;
-    a.split = PAIR ? 1 : plan.split;
+    a.split = SPLIT ? plan.split : 1;
     const int nkb = (K + kKBytes - 1) / kKBytes;
     const int ot = PAIR ? 2 * kTileRows : kTileRows;
     a.n_o = static_cast<int>((static_cast<int64_t>(N) + ot - 1) / ot);
@@ -656,24 +670,27 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     if (PAIR) {
         // the clusters' shared memory barely depends on the plan: one count serves all
         cudaLaunchConfig_t most = cfg;
-        most.dynamicSmemBytes = kSmemMax + kTailBytes + 1024;
-        grid = 2 * std::min<int64_t>(
-                       tiles, resident_pairs(a8_qgemm_kernel<FMT, YT, PAIR, G>, most, dev, pairs_cache));
+        most.dynamicSmemBytes = kSmemMax + tail_bytes(G) + 1024;
+        grid = 2 * std::min<int64_t>(tiles, resident_pairs(kernel, most, dev, pairs_cache));
     } else if (G > 1 && a.split == 1) {
         grid = std::min<int64_t>(tiles, sm_count());
     }
     const int64_t share = (tiles * csize + grid - 1) / grid;   // tiles a CTA or cluster
     a.alt = share > 1;
     // Clusters wait for their peers, so none of their CTAs may wait in tcgen05.alloc
-    // for another cluster's: pairs leave no registers beside them on an SM, and at
-    // most three CTAs of G = 1 fit, with 128 columns each at most.
+    // for another cluster's: pairs leave no registers beside them on an SM, and a CTA
+    // of a split takes a larger part of the shared memory than of the 512 columns
+    // (128, 64, 32 columns: at least 98, 75, 52 KB of 227).
     a.acc_cols = 32;
     while (a.acc_cols < (a.alt ? 2 : 1) * a.bn) a.acc_cols *= 2;
+    const int sbytes = stage_bytes(a.bn, PAIR), red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
+    const int fit = std::max(2, ((G == 1 ? kSmemSmall : kSmemMax) - red) / sbytes);
     a.stages = static_cast<int>(std::min<int64_t>(
-        std::min(kMaxStages, (G == 1 ? kSmemSmall : kSmemMax) / stage_bytes(a.bn, PAIR)),
+        std::min(kMaxStages, fit),
         share * ((((nkb + a.split - 1) / a.split) + stage_atoms(PAIR) - 1) / stage_atoms(PAIR))));
-    a.tail_off = ring_bytes(a, PAIR);
-    cfg.dynamicSmemBytes = a.tail_off + kTailBytes + 1024;
+    a.red_off = a.stages * sbytes;
+    a.tail_off = a.red_off + red;
+    cfg.dynamicSmemBytes = a.tail_off + tail_bytes(G) + 1024;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -687,16 +704,20 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, a8_qgemm_kernel<FMT, YT, PAIR, G>, w_map, x_map, a, ctl);
+    return cudaLaunchKernelEx(&cfg, kernel, w_map, x_map, a, ctl);
 }
 
 template <int FMT, typename YT>
 cudaError_t launch_a8_p(const A8Plan &p, const void *Xq, const float *xs, const void *Wq,
                         const float *wsc, const float *bias, void *Y, int M, int N, int K,
                         DevCtl *ctl, cudaStream_t s) {
-    if (p.pair) return launch_a8<FMT, YT, true, 4>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
-    if (p.small) return launch_a8<FMT, YT, false, 1>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
-    return launch_a8<FMT, YT, false, 4>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    if (p.pair)
+        return launch_a8<FMT, YT, true, 4, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    if (p.split > 1)
+        return launch_a8<FMT, YT, false, 1, true>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    if (p.small)
+        return launch_a8<FMT, YT, false, 1, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    return launch_a8<FMT, YT, false, 4, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
 }
 
 template <int FMT>
