@@ -749,20 +749,30 @@ int sm_count() {
     return n;
 }
 
-// The plan of least estimated time.  The estimate (in us, beyond the launch):
-// an SM takes in 128-byte rows of operands at one per 1.24 ns, which is slower
-// than the MMAs they feed; a tile's epilogue takes 0.47 + 0.0067 bn; a split adds
-// its cluster and the sum over distributed shared memory, a pair its
-// handshakes; in a walk of tiles the shorter of load and epilogue hides by 70 %.  Fitted to 1.9 thousand timings of M = 1 to 4096 against eight
-// weight shapes from 512 x 512 to 8192 x 8192; over those shapes the plan taken
-// is on average 1.8 % slower than the best of them, at most 25 %.
+// The plan of least estimated time.  The estimate (in us, beyond the 1.76 that a launch
+// takes): an SM takes in 128-byte rows of operands at one per 0.98 to 1.16 ns (the
+// smaller ring of G = 1 less well), which is slower than the MMAs they feed; a tile's
+// epilogue takes 0.04 + 0.0094 bn; a split adds its cluster and the exchange of partial
+// sums, a pair its handshakes; in a walk of tiles load and epilogue hide little of each
+// other, since both are bytes between the SM and L2.  Rows whose length is no
+// multiple of 128 bytes lie across two L2 lines a piece and count 1.5 times (20001 x
+// 2048 x 1040 bf16 47 us, K = 1024 36).  Weights of more than 60 MB come from HBM,
+// faster the more CTAs ask for them (16 x 8192 x 8192 on 64, 128 and 256 CTAs: 22, 16
+// and 14.7 us).  Fitted to 1.9 thousand timings; against every plan at M = 1 to 4096,
+// twelve weight shapes from 512 x 64 to 8192 x 8192 and both formats the one taken is on
+// average 1 % slower than the best, at most 20 %.
 A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
     const int nkb = (K + kKBytes - 1) / kKBytes;
     const int n_o = static_cast<int>((static_cast<int64_t>(N) + kTileRows - 1) / kTileRows);
     const int n_op = (n_o + 1) / 2;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    const auto rows_us = [&](int rows, int kb) { return 0.001235f * static_cast<float>(rows) * kb; };
-    const auto epi_us = [](int bn) { return 0.47f + 0.0067f * static_cast<float>(bn); };
+    const float lines = K % kKBytes ? 1.5f : 1.f;
+    const auto rows_us = [=](float us, int rows, int kb) {
+        return lines * us * static_cast<float>(rows) * static_cast<float>(kb);
+    };
+    const auto epi_us = [](int bn) { return 0.04f + 0.0094f * static_cast<float>(bn); };
+    const float mbytes = 1e-6f * static_cast<float>(N) * static_cast<float>(K);
+    const auto hbm_us = [&](float tbps) { return mbytes > 60.f ? mbytes / tbps : 0.f; };
     A8Plan best = {16, 1, 0, 1, 0};
     float least = 1e30f;
     const auto offer = [&](const A8Plan &p, float us) {
@@ -777,12 +787,16 @@ A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
         const int64_t tiles = n_o * up(std::max(M, 1), bn);
         for (int log = 0; log < 4; ++log) {
             const int split = 1 << log;
-            constexpr float kCluster[4] = {0.f, 0.42f, 0.26f, 0.61f};
+            constexpr float kCluster[4] = {0.f, 0.59f, 0.58f, 0.75f};
             if (split > nkb || tiles * split > 6 * sms) break;
             const float per = static_cast<float>(up(tiles * split, sms));
+            const float load = per * rows_us(0.00116f, kTileRows + bn, (nkb + split - 1) / split);
+            const float hbm = hbm_us(n_o * split * 2 >= 3 * sms   ? 5.9f
+                                     : n_o * split * 4 >= 3 * sms ? 5.1f
+                                                                  : 3.4f);
             offer({bn, split, 0, 1, 0},
-                  per * rows_us(kTileRows + bn, (nkb + split - 1) / split) + 0.34f * (per - 1.f) +
-                      epi_us(bn) * (split > 1 ? 2.34f : 1.f) + kCluster[log]);
+                  std::max(load, hbm) + 0.84f * (per - 1.f) + epi_us(bn) +
+                      (split > 1 ? 0.025f * static_cast<float>(bn) : 0.f) + kCluster[log]);
         }
     }
     // persistent tiles, on single CTAs and on pairs
@@ -790,31 +804,37 @@ A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
         for (int bn = 64; bn <= 256 && bn <= std::max<int64_t>(64, up(M, 32) * 32); bn += 32) {
             const int64_t tiles = (pair ? n_op : n_o) * up(std::max(M, 1), bn);
             const float per = static_cast<float>(up(tiles, pair ? sms / 2 : sms));
-            const float load = rows_us(kTileRows + (pair ? bn / 2 : bn), nkb), epi = epi_us(bn);
+            const float load = pair ? rows_us(0.00116f, kTileRows + bn / 2, nkb)
+                                    : rows_us(0.00098f, kTileRows + bn, nkb);
+            const float epi = epi_us(bn);
+            const float walk =
+                load + (per - 1.f) * (std::max(load, epi) + 0.95f * std::min(load, epi));
             offer({bn, 1, pair, 0, 0},
-                  load + (per - 1.f) * (std::max(load, epi) + 0.3f * std::min(load, epi)) + epi +
-                      (pair ? 0.9f : 0.f));
+                  std::max(walk, hbm_us(4.8f)) + epi + 0.2f + (pair ? 0.98f : 0.f));
         }
-    // A few rows on the CUDA cores, 1 or 4 weight rows a warp (us less 2.75, which
-    // the tensor kernels take to set up): a 512-byte step of K costs a load's
-    // latency, a byte of weights its load or its arithmetic.  The tensor path takes
-    // weights from HBM at 5.4 TB/s at most.  Measured, us, CUDA cores and tensor
-    // cores: M = 1, int8, 512 x 512: 1.5 and 3.5, 512 x 2048 (K): 2.0 and 4.8, 8192 x
-    // 8192: 12.2 and 15.2; M = 8, 4096 x 4096: 6.6 and 6.2; M = 80, 512 x 512: 2.4 and
-    // 3.7, 2048 x 512: 5.5 and 3.7; e4m3, M = 1, 8192 x 8192: 17.1 and 15.6; M = 80,
-    // 512 x 512: 3.6 and 3.8.
+    // A few rows on the CUDA cores, 1 or 4 weight rows a warp (us beyond 1.76): a
+    // 512-byte step of K costs a load's latency, a byte of weights its load or its
+    // arithmetic, in whole steps.  One weight row a warp where four would leave SMs without
+    // warps, or where the loads are the time.  Measured, us, CUDA cores and tensor
+    // cores: M = 1, int8, 512 x 512: 1.5 and 2.6, 512 x 2048 (K): 1.9 and 3.3, 8192 x
+    // 8192: 12.2 and 14.0; M = 8, 4096 x 4096: 6.7 and 4.6; M = 80, 512 x 512: 2.4 and
+    // 2.7, 2048 x 512: 5.5 and 2.8; e4m3, M = 1, 8192 x 8192: 17.1 and 14.1; M = 80,
+    // 512 x 512: 3.6 and 2.9; one and four weight rows, M = 8, int8: 512 x 2048 2.7
+    // and 3.1, 4096 x 512 2.9 and 2.4.
     if (M >= 1 && M <= 128) {
-        const float mbytes = 1e-6f * static_cast<float>(N) * static_cast<float>(K);
-        const float steps = static_cast<float>(up(K, 512));
-        least = std::max(least, mbytes / 5.4f);
+        const int64_t steps = up(K, 512), groups = up(M, 8);
+        const float step_us = static_cast<float>(steps - 1);
+        const float mb = 1e-6f * static_cast<float>(N) * static_cast<float>(512 * steps);
         const bool q8 = fmt == kFmtQ8;
-        if (M <= 4 && !(K <= 512 && N >= 2048)) {
-            const float byte_us = q8 ? 0.12f + 0.031f * M : 0.14f + 0.089f * M;
-            offer({8, 1, 0, 0, 1}, -1.55f + 0.08f * steps + byte_us * mbytes);
+        if (M <= 4 && !(K < 1024 && N > 2048)) {
+            const float byte_us = q8 ? 0.08f + 0.031f * M : 0.14f + 0.089f * M;
+            offer({8, 1, 0, 0, 1},
+                  -0.48f + 0.08f * step_us + std::max(byte_us * mb, hbm_us(5.9f)));
         } else {
-            const float work = mbytes * static_cast<float>(M <= 4 ? M : up(M, 8) * 8);
-            offer({8, 1, 0, 0, 4}, q8 ? -1.4f + 0.3f * (steps - 1.f) + (K <= 512 ? 0.045f : 0.03f) * work
-                                      : -1.15f + 0.7f * (steps - 1.f) + 0.085f * work);
+            const float work = lines * mb * static_cast<float>(M <= 4 ? M : 8 * groups);
+            offer({8, 1, 0, 0, M > 4 && N * groups <= 1024 ? 1 : 4},
+                  q8 ? -0.41f + 0.3f * step_us + (K <= 512 ? 0.045f : 0.03f) * work
+                     : -0.16f + 0.7f * step_us * (M <= 4 ? 0.125f * M : 1.f) + 0.085f * work);
         }
     }
     return best;
