@@ -529,8 +529,9 @@ cudaError_t launch_rows_nv(const RowArgs &a, int tpr, cudaStream_t s) {
     return launch_rows<T, MODE, FMT, 1024, NV>(a, s);
 }
 
-// Threads a row and vectors a thread.  Few rows: 1 vector, for the shortest chain
-// (80 x 512 bf16 norm: 1.7 us, with 2 it takes 2.4).  Many rows: 3 where that
+// Threads a row and vectors a thread.  Few rows, up to half of the threads that the
+// device holds: 1 vector, for the shortest chain (80 x 512 bf16 norm: 1.7 us, with 2
+// 2.4; 1001 x 512: 2.2 and 2.5; beyond, 1180 x 1024 fp32: 3.4 and 3.1).  Many rows: 3 where that
 // leaves fewer threads idle than a power of two, else what keeps most bytes in
 // flight for the registers it takes.  16-bit types 2: 65536 x 2048 bf16 gate 107
 // us (1: 119, 4: 107), norm 144 (1: 152, 4: 159).  fp32 quantization 4: 65536 x 512
@@ -544,7 +545,8 @@ cudaError_t launch_rows_k(const RowArgs &a, cudaStream_t s) {
     const int vecs = a.K / Vec<T>::n;
     int room = 32;                                    // a power of two that holds the row
     while (room < vecs) room *= 2;
-    if (room <= 512 && a.M <= 8 * sm_count()) return launch_rows_nv<T, MODE, FMT, 1>(a, room, s);
+    if (room <= 512 && static_cast<int64_t>(a.M) * room <= 1024 * sm_count())
+        return launch_rows_nv<T, MODE, FMT, 1>(a, room, s);
     if (room >= 128 && room <= 4096 && 4 * vecs <= 3 * room)
         return launch_rows_nv<T, MODE, FMT, 3>(a, room / 4, s);
     if (room == 32 || (kWide && MODE == kModeNorm && room <= 128))
