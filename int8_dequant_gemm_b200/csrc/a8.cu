@@ -25,7 +25,8 @@
 //   - persistent tiles of 128 weight rows x bn activation rows, one CTA each,
 //     two accumulators so that a tile's epilogue runs under the next one's MMAs;
 //   - the same on CTA pairs (PAIR): one cta_group::2 MMA over 256 weight rows,
-//     each CTA staging its own 128 weight rows and half of the activation rows;
+//     each CTA staging its own 128 weight rows and half of the activation rows,
+//     which stay for all weight tiles where K is short (RES);
 //   - few tiles: K split over a cluster of `split` CTAs (SPLIT), one tile a cluster,
 //     partial sums sent through distributed shared memory and added in rank order.
 #include <cuda_bf16.h>
@@ -54,6 +55,7 @@ constexpr int stage_atoms(int pair) { return pair ? 1 : 2; }
 constexpr int epi_warp0(int G) { return G == 1 ? 2 : 4; }
 constexpr int cta_threads(int G) { return (epi_warp0(G) + 4 * G) * 32; }
 constexpr int kMaxStages = 8;
+constexpr int kResAtoms = 9;                       // K atoms of activations that stay (RES)
 constexpr int kBand = 8;                           // activation tiles walked together
 constexpr uint16_t kBoth = 3;                      // multicast mask: both CTAs of a pair
 constexpr int kSmemMax = 200 * 1024;               // ring of stages
@@ -67,9 +69,10 @@ struct A8Args {
     int n_o, n_m;            // weight tiles, activation tiles
     int acc_cols;
     int alt;                 // two epilogue sets take turns
+    int res_off;             // after the ring, RES: the activations' atoms
     int red_off;             // after the ring, split: partial sums of this rank's columns,
                              // [rank][column][128]
-    int tail_off;            // after both: each epilogue warp's activation
+    int tail_off;            // after these: each epilogue warp's activation
                              // scales [4 G][2][kWarpWords], barriers and words
 };
 
@@ -80,10 +83,12 @@ __host__ __device__ constexpr int stage_bytes(int bn, int pair) {
     return stage_atoms(pair) * atom_bytes(bn, pair);
 }
 
+// RES: the K atoms of a CTA's activation rows.
+__host__ inline int res_bytes(int bn, int nkb) { return nkb * (bn / 2) * kKBytes; }
 constexpr int kWarpRows = 128;                     // activation rows of a tile an epilogue warp takes
 constexpr int kWarpWords = kWarpRows + 64;         // their scales, then each lane's ws and bias
 constexpr int scale_bytes(int G) { return 4 * G * 2 * kWarpWords * 4; }
-constexpr int tail_bytes(int G) { return scale_bytes(G) + (2 * kMaxStages + 5) * 8 + 16; }
+constexpr int tail_bytes(int G) { return scale_bytes(G) + (2 * kMaxStages + 2 * kResAtoms + 5) * 8 + 16; }
 
 // Instruction descriptors (A and B K-major): accumulator s32 (2) or f32 (1),
 // operand type 1 = s8 of kind::i8, 0 = e4m3 of kind::f8f6f4.
@@ -253,10 +258,16 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[kChunk], YT *y, 
 
 // Tile t of the walk: bands of kBand activation tiles, all weight tiles of a
 // band, activation tile fastest.  The tiles that run at once then share few
-// operand rows, which stay in L2.
+// operand rows, which stay in L2.  `res`: all weight tiles of one activation tile
+// after another, each group of CTAs a contiguous share.
 struct TileAt {
     int m, o;
-    __device__ TileAt(int t, int n_m, int n_o) {
+    __device__ TileAt(int t, int n_m, int n_o, bool res) {
+        if (res) {
+            m = t / n_o;
+            o = t - m * n_o;
+            return;
+        }
         const int band = t / (kBand * n_o);
         const int m0 = band * kBand, mb = min(kBand, n_m - m0);
         const int r = t - band * kBand * n_o;
@@ -265,7 +276,11 @@ struct TileAt {
     }
 };
 
-template <int FMT, typename YT, bool PAIR, int G, bool SPLIT>
+__host__ __device__ inline int share_of(int n, int i, int parts) {
+    return static_cast<int>(static_cast<int64_t>(n) * i / parts);
+}
+
+template <int FMT, typename YT, bool PAIR, int G, bool SPLIT, bool RES>
 __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     a8_qgemm_kernel(const __grid_constant__ CUtensorMap w_map,
                     const __grid_constant__ CUtensorMap x_map, const A8Args a, DevCtl *ctl) {
@@ -279,7 +294,8 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(tail + scale_bytes(G));
     uint64_t *empty = full + kMaxStages;
     uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *x_full = drain + 1, *x_empty = x_full + kResAtoms;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_empty + kResAtoms);
     volatile uint32_t *failed = tmem_slot + 1;     // split: a rank has no sum
 
     // (warp: by a shuffle, so that the compiler knows it to be the same in all lanes)
@@ -292,9 +308,14 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     const int nkb = (a.K + kKBytes - 1) / kKBytes;
     const int kb0 = SPLIT ? nkb * rank / split : 0, kb1 = SPLIT ? nkb * (rank + 1) / split : nkb;
     const int n_tiles = a.n_o * a.n_m;
-    const int first = static_cast<int>(blockIdx.x) / csize;
-    const int step = static_cast<int>(gridDim.x) / csize;
-    const int abytes = atom_bytes(a.bn, PAIR), sbytes = kAtoms * abytes;
+    // tiles first, first + step, ... below end
+    const int group = static_cast<int>(blockIdx.x) / csize;
+    const int groups_n = static_cast<int>(gridDim.x) / csize;
+    const int first = RES ? share_of(n_tiles, group, groups_n) : group;
+    const int end = RES ? share_of(n_tiles, group + 1, groups_n) : n_tiles;
+    const int step = RES ? 1 : groups_n;
+    const int abytes = RES ? kABytes : atom_bytes(a.bn, PAIR), sbytes = kAtoms * abytes;
+    const int xbytes = atom_bytes(a.bn, PAIR) - kABytes;
     const unsigned long long *lim = &ctl->wait_ns;
     const bool inject = leader && ctl->inject;     // read before the wait below
 
@@ -307,6 +328,11 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * (a.alt ? kEpiWarps / 2 : kEpiWarps));
         }
+        if (RES)
+            for (int i = 0; i < nkb; ++i) {
+                mbar_init(&x_full[i], 1);
+                mbar_init(&x_empty[i], 1);
+            }
         mbar_init(drain, 1);
         *failed = 0;
         fence_mbar_init();
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     bool ok = true;
     float wsc[4] = {1.f, 1.f, 1.f, 1.f}, bo[4] = {};       // of the split-K sum's weight rows
     if (SPLIT && warp >= kEpiWarp0) {
-        const TileAt at(first, a.n_m, a.n_o);
+        const TileAt at(first, a.n_m, a.n_o, RES);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int n = at.o * kTileRows + 4 * lane + i;
@@ -355,13 +381,26 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         // ============================================================ TMA
         // (Test hook: with `inject` the first weight box is never requested.)
         bool good = true;
-        int s = 0, j = 0;
+        int s = 0, j = 0, x_loads = 0;
         uint32_t par = 1;
-        for (int t = first; t < n_tiles; t += step) {
-            const TileAt at(t, a.n_m, a.n_o);
+        for (int t = first; t < end; t += step) {
+            const TileAt at(t, a.n_m, a.n_o, RES);
             const int oy = (PAIR ? 2 * at.o + rank : at.o) * kTileRows;
             const int my = at.m * a.bn + (PAIR ? rank * (a.bn / 2) : 0);
+            const bool x_new = RES && (t == first || at.o == 0);
+            if (x_new) ++x_loads;
             for (int kb = kb0; kb < kb1; kb += kAtoms, ++j) {
+                if (x_new) {
+                    // this atom of the last activation tile has been multiplied
+                    if (good && x_loads > 1)
+                        good = mbar_wait(&x_empty[kb], static_cast<uint32_t>(x_loads) & 1u, lim);
+                    if (elect_one() && good) {
+                        const uint32_t cbar = cluster_map(smem_addr(&x_full[kb]), 0);
+                        if (leader) mbar_expect_tx(&x_full[kb], static_cast<uint32_t>(2 * xbytes));
+                        tma_load_2d_pair(base + static_cast<uint32_t>(a.res_off + kb * xbytes), &x_map,
+                                         kb * kKBytes, my, cbar);
+                    }
+                }
                 if (good && j >= a.stages) good = mbar_wait(&empty[s], par, lim);
                 const int atoms = min(kAtoms, kb1 - kb);
                 const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * atoms * abytes);
@@ -376,7 +415,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                         const bool skip = inject && j == 0 && u == 0;
                         if (PAIR) {
                             if (!skip) tma_load_2d_pair(dst, &w_map, x, oy, cbar);
-                            tma_load_2d_pair(dst + kABytes, &x_map, x, my, cbar);
+                            if (!RES) tma_load_2d_pair(dst + kABytes, &x_map, x, my, cbar);
                         } else {
                             if (!skip) tma_load_2d(dst, &w_map, x, oy, &full[s]);
                             tma_load_2d(dst + kABytes, &x_map, x, my, &full[s]);
@@ -399,6 +438,9 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                 if (good && !(last_j == 0 && inject))
                     mbar_wait(&full[i], static_cast<uint32_t>(last_j / a.stages) & 1u, lim);
             }
+            if (RES)
+                for (int kb = 0; kb < nkb && x_loads > 0 && good; ++kb)
+                    mbar_wait(&x_full[kb], static_cast<uint32_t>(x_loads - 1) & 1u, lim);
         }
         ok = good;
     } else if (warp == 1) {
@@ -406,19 +448,27 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         if (leader) {
             const uint32_t idesc = idesc_8bit(FMT, (PAIR ? 2 : 1) * kTileRows, a.bn);
             bool good = true;
-            int s = 0, n_local = 0;
+            int s = 0, n_local = 0, x_loads = 0;
             uint32_t par = 0;
-            for (int t = first; t < n_tiles; t += step, ++n_local) {
+            for (int t = first; t < end; t += step, ++n_local) {
+                const int o_at = RES ? t % a.n_o : 0;
+                const bool x_new = RES && (t == first || o_at == 0);
+                const bool x_last = RES && (t + 1 == end || o_at == a.n_o - 1);
+                if (x_new) ++x_loads;
                 const int b = n_local & 1;
                 if (good && n_local >= 2)
                     good = mbar_wait(&acc_empty[b], static_cast<uint32_t>((n_local / 2) - 1) & 1u,
                                      lim);
                 const uint32_t d = tmem + static_cast<uint32_t>(b * a.bn);
                 for (int kb = kb0; kb < kb1; kb += kAtoms) {
+                    if (x_new && good)
+                        good = mbar_wait(&x_full[kb], static_cast<uint32_t>(x_loads - 1) & 1u, lim);
                     if (good) good = mbar_wait(&full[s], par, lim);
                     tc_fence_after_sync();
                     const uint32_t st = base + static_cast<uint32_t>(s * sbytes);
-                    const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
+                    const uint64_t ad = sw128_kmajor_desc(st);
+                    const uint64_t bd = sw128_kmajor_desc(
+                        RES ? base + static_cast<uint32_t>(a.res_off + kb * xbytes) : st + kABytes);
                     const uint64_t next = static_cast<uint64_t>(abytes >> 4);
                     // K left in this CTA's slice; the rest of the last atom is zero fill
                     const int left = min(a.K, kb1 * kKBytes) - kb * kKBytes;
@@ -431,6 +481,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                                                     (kb > kb0 || kk > 0) ? 1u : 0u);
                         if (PAIR) tc_commit_pair_mc(&empty[s], kBoth);
                         else tc_commit(&empty[s]);
+                        if (x_last) tc_commit_pair_mc(&x_empty[kb], kBoth);
                     }
                     if (++s == a.stages) {
                         s = 0;
@@ -471,8 +522,8 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         // wait gave up would not come to.
         uint32_t xs_w = smem_addr(xs_s) + ew * (2 * kWarpWords * 4), flip = 0;
         auto fetch = [&](int t, uint32_t to) {
-            if (SPLIT || t >= n_tiles) return;
-            const TileAt at(t, a.n_m, a.n_o);
+            if (SPLIT || t >= end) return;
+            const TileAt at(t, a.n_m, a.n_o, RES);
 #pragma unroll
             for (int i = 0; i < kWarpRows / 32; ++i) {
                 const int c = 32 * h + chunk_step * i + lane, m = at.m * a.bn + c;
@@ -490,8 +541,8 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         fetch(first + set * step, xs_w);
         if (SPLIT) cluster_wait();      // the peers have started
         int n_local = set;
-        for (int t = first + set * step; t < n_tiles && ok; t += turn * step, n_local += turn) {
-            const TileAt at(t, a.n_m, a.n_o);
+        for (int t = first + set * step; t < end && ok; t += turn * step, n_local += turn) {
+            const TileAt at(t, a.n_m, a.n_o, RES);
             const int b = n_local & 1;
             const int m0 = at.m * a.bn;
             const int mlim = min(a.bn, a.M - m0);
@@ -586,7 +637,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         // one cluster barrier orders them (80 x 512 x 2048 e4m3: 3.7 us; with the sums
         // read from the peers, between two barriers, 4.6).  Rank r of the cluster adds and stores columns [bn r / split,
         // bn (r + 1) / split): all ranks' partial sums of them, in rank order.
-        const TileAt at(first, a.n_m, a.n_o);
+        const TileAt at(first, a.n_m, a.n_o, RES);
         YT *const Y = static_cast<YT *>(a.Y);
         float nf = 0.f;
         const int own = a.bn / split, m0 = at.m * a.bn + rank * own;
@@ -630,7 +681,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     }
 }
 
-template <int FMT, typename YT, bool PAIR, int G, bool SPLIT>
+template <int FMT, typename YT, bool PAIR, int G, bool SPLIT, bool RES>
 cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const void *Wq,
                       const float *wsc, const float *bias, void *Y, int M, int N, int K,
                       DevCtl *ctl, cudaStream_t st) {
@@ -639,7 +690,7 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto kernel = a8_qgemm_kernel<FMT, YT, PAIR, G, SPLIT>;
+    const auto kernel = a8_qgemm_kernel<FMT, YT, PAIR, G, SPLIT, RES>;
     if ((e = smem_attr_once(kernel, 227 * 1024, dev, attr_done)) != cudaSuccess) return e;
     A8Args a = {};
     a.xs = xs;
@@ -685,12 +736,14 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     // (128, 64, 32 columns: at least 98, 75, 52 KB of 227).
     a.acc_cols = 32;
     while (a.acc_cols < (a.alt ? 2 : 1) * a.bn) a.acc_cols *= 2;
-    const int sbytes = stage_bytes(a.bn, PAIR), red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
-    const int fit = std::max(2, ((G == 1 ? kSmemSmall : kSmemMax) - red) / sbytes);
+    const int sbytes = RES ? kABytes : stage_bytes(a.bn, PAIR);
+    const int res = RES ? res_bytes(a.bn, nkb) : 0, red = a.split > 1 ? a.bn * kTileRows * 4 : 0;
+    const int fit = std::max(2, ((G == 1 ? kSmemSmall : kSmemMax) - red - res) / sbytes);
     a.stages = static_cast<int>(std::min<int64_t>(
         std::min(kMaxStages, fit),
         share * ((((nkb + a.split - 1) / a.split) + stage_atoms(PAIR) - 1) / stage_atoms(PAIR))));
-    a.red_off = a.stages * sbytes;
+    a.res_off = a.stages * sbytes;
+    a.red_off = a.res_off + res;
     a.tail_off = a.red_off + red;
     cfg.dynamicSmemBytes = a.tail_off + tail_bytes(G) + 1024;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -709,17 +762,34 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
     return cudaLaunchKernelEx(&cfg, kernel, w_map, x_map, a, ctl);
 }
 
+// Pairs: an activation tile stays in shared memory for all weight tiles (RES), which
+// takes half of the operand bytes off the way from L2, where the other operand's ring
+// keeps enough stages and the weights stay in L2.  Rows that are no multiple of 128
+// bytes gain most: a piece of them lies across two L2 lines.  us, streamed and
+// kept, bf16: 20001 x 2003 x 1040 55.6 and 49.6, 32768 x 2048 x 400 43.7 and 38.8, 65536 x 4096 x
+// 512 150 and 143, 16384 x 4096 x 768 46.8 and 45.0; 20001 x 2048 x 1024 35.7 and 37.8
+// (four stages left); fp32: 16384 x 2048 x 528 33.7 and 30.9, 16384 x 4096 x 768 65.0
+// and 60.6; 32768 x 2048 x 512 52.6 and 57.9 (bound by the stores of Y, which follow
+// each other more closely in bands); bf16 65536 x 512 x 512 21.8 and 22.5 (two tiles).
+bool activations_stay(int N, int K, size_t y_bytes) {
+    const int nkb = (K + kKBytes - 1) / kKBytes;
+    if (nkb > kResAtoms || static_cast<int64_t>(N) * K > (int64_t(32) << 20)) return false;
+    return K % kKBytes != 0 || (N >= 1024 && nkb <= 6 && (y_bytes == 2 || nkb > 4));
+}
+
 template <int FMT, typename YT>
 cudaError_t launch_a8_p(const A8Plan &p, const void *Xq, const float *xs, const void *Wq,
                         const float *wsc, const float *bias, void *Y, int M, int N, int K,
                         DevCtl *ctl, cudaStream_t s) {
+    if (p.pair && activations_stay(N, K, sizeof(YT)))
+        return launch_a8<FMT, YT, true, 4, false, true>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
     if (p.pair)
-        return launch_a8<FMT, YT, true, 4, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+        return launch_a8<FMT, YT, true, 4, false, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
     if (p.split > 1)
-        return launch_a8<FMT, YT, false, 1, true>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+        return launch_a8<FMT, YT, false, 1, true, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
     if (p.small)
-        return launch_a8<FMT, YT, false, 1, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
-    return launch_a8<FMT, YT, false, 4, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+        return launch_a8<FMT, YT, false, 1, false, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
+    return launch_a8<FMT, YT, false, 4, false, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
 }
 
 template <int FMT>

@@ -282,7 +282,8 @@ SIZES = [(1, 1, 16), (1, 4096, 512), (2, 7, 32), (15, 130, 144), (16, 128, 128),
          (257, 513, 640), (300, 512, 2048), (513, 384, 128), (1000, 1003, 1040), (1024, 4096, 512),
          (2049, 512, 2064), (4096, 512, 512), (2500, 1000, 512), (3001, 2000, 400),
          (5003, 1003, 1040), (4100, 2200, 2048), (9000, 515, 256), (9, 5000, 2048), (520, 4999, 1024),
-         (3, 4097, 512), (4, 131, 8208), (5, 512, 2048), (8, 515, 528), (8, 4100, 4096), (2, 6001, 1040)]
+         (3, 4097, 512), (4, 131, 8208), (5, 512, 2048), (8, 515, 528), (8, 4100, 4096), (2, 6001, 1040), (6000, 2000, 400), (9000, 2048, 640),
+         (9001, 2003, 1040), (7001, 2050, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -494,7 +495,8 @@ def test_explicit_stream_and_one_buffer_reused(rtq):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M,N,K", [(128, 129, 4112), (100, 30000, 128), (2500, 1000, 512), (5003, 1003, 1040)])
+@pytest.mark.parametrize("M,N,K", [(128, 129, 4112), (100, 30000, 128), (2500, 1000, 512), (5003, 1003, 1040),
+                                   (4100, 2200, 2048), (9000, 2048, 640)])
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
 def test_injected_missing_box_times_out_and_recovers(rtq, M, N, K, fmt):
     xc, xs, wc, ws, b = operands(fmt, M, N, K, seed=13)
