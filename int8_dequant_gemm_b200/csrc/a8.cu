@@ -15,8 +15,10 @@
 // 128-byte segments of Y for every N, and few activation rows cost few columns.
 // Measured and not kept: activation rows in lanes with 32-byte stores (a quarter
 // of the store instructions; 276 against 204 us for 65536 x 4096 x 512 into
-// fp32, 181 against 175 into bf16), and tiles of Y staged in shared memory and
-// stored by TMA (19.8 against 17.5 us for 4096 x 4096 x 512).
+// fp32, 181 against 175 into bf16, then), and tiles of Y staged in shared memory
+// and stored by TMA (19.8 against 17.5 us for 4096 x 4096 x 512).
+// What bounds large products is bytes between L2 and the SMs, 10 to 12 TB/s of operands
+// and Y together (65536 x 4096 x 512: bf16 143 us, fp32 205; 8192^3 365).
 //
 // Roles (20 warps): warp 0 TMA, warp 1 MMA issue, warps 4-19 epilogue (four per
 // TMEM lane quadrant); warps 2-3 idle.
@@ -50,8 +52,9 @@ constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights an atom
 // 12.3 -> 10.4; 8192^3 on pairs 369 -> 381).
 constexpr int stage_atoms(int pair) { return pair ? 1 : 2; }
 // Epilogue groups G of four warps, one per TMEM lane quadrant: 4 for persistent
-// tiles, 1 where a CTA has one narrow tile (192 threads and at most half an
-// SM's registers and shared memory, so the next kernel's CTA starts beside it).
+// tiles, 1 where a CTA has one narrow tile (192 threads and, but for the widest
+// splits, at most half an SM's registers and shared memory, so the next kernel's CTA
+// starts beside it).
 constexpr int epi_warp0(int G) { return G == 1 ? 2 : 4; }
 constexpr int cta_threads(int G) { return (epi_warp0(G) + 4 * G) * 32; }
 constexpr int kMaxStages = 8;
@@ -766,9 +769,9 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
 // takes half of the operand bytes off the way from L2, where the other operand's ring
 // keeps enough stages and the weights stay in L2.  Rows that are no multiple of 128
 // bytes gain most: a piece of them lies across two L2 lines.  us, streamed and
-// kept, bf16: 20001 x 2003 x 1040 55.6 and 49.6, 32768 x 2048 x 400 43.7 and 38.8, 65536 x 4096 x
-// 512 150 and 143, 16384 x 4096 x 768 46.8 and 45.0; 20001 x 2048 x 1024 35.7 and 37.8
-// (four stages left); fp32: 16384 x 2048 x 528 33.7 and 30.9, 16384 x 4096 x 768 65.0
+// kept, bf16: 20001 x 2003 x 1040 55.6 and 49.6, 32768 x 2048 x 400 43.7 and 38.8,
+// 65536 x 4096 x 512 150 and 143, 16384 x 4096 x 768 46.8 and 45.0; 20001 x 2048 x
+// 1024 35.7 and 37.8 (four stages left); fp32: 16384 x 2048 x 528 33.7 and 30.9, 16384 x 4096 x 768 65.0
 // and 60.6; 32768 x 2048 x 512 52.6 and 57.9 (bound by the stores of Y, which follow
 // each other more closely in bands); bf16 65536 x 512 x 512 21.8 and 22.5 (two tiles).
 bool activations_stay(int N, int K, size_t y_bytes) {
