@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                                            static_cast<uint32_t>(r)), 1);
     }
     tc_fence_before_sync();
+    if (SPLIT) __syncwarp();
     if (PAIR || SPLIT) cluster_sync();
     else __syncthreads();
     if (SPLIT && warp >= kEpiWarp0 && *failed == 0) {
