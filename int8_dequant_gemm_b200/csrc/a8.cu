@@ -61,8 +61,8 @@ constexpr int kMaxStages = 8;
 constexpr int kResAtoms = 9;                       // K atoms of activations that stay (RES)
 constexpr int kBand = 8;                           // activation tiles walked together
 constexpr uint16_t kBoth = 3;                      // multicast mask: both CTAs of a pair
-constexpr int kSmemMax = 200 * 1024;               // ring of stages
-constexpr int kSmemSmall = 100 * 1024;             // the same for G = 1
+constexpr int kSmemMax = 200 * 1024;               // ring of stages (RES: and the activations)
+constexpr int kSmemSmall = 100 * 1024;             // ring and partial sums for G = 1
 constexpr int kChunk = 16;                         // activation rows an epilogue warp takes at once
 
 struct A8Args {
@@ -639,8 +639,9 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         // ============================================================ split-K sum
         // Each rank has sent its peers their columns, a store a column and warp, and
         // one cluster barrier orders them (80 x 512 x 2048 e4m3: 3.7 us; with the sums
-        // read from the peers, between two barriers, 4.6).  Rank r of the cluster adds and stores columns [bn r / split,
-        // bn (r + 1) / split): all ranks' partial sums of them, in rank order.
+        // read from the peers, between two barriers, 4.6).  Rank r of the cluster adds
+        // and stores columns [bn r / split, bn (r + 1) / split): all ranks' partial sums
+        // of them, in rank order.
         const TileAt at(first, a.n_m, a.n_o, RES);
         YT *const Y = static_cast<YT *>(a.Y);
         float nf = 0.f;

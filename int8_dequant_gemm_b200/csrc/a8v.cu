@@ -4,8 +4,8 @@
 // through shared memory and TMEM.
 //
 // A warp takes RW weight rows and MT activation rows and walks K in 512-byte
-// steps, 16 bytes of every row a lane; the activation rows come from L1.  int8: four-way integer dot
-// products, exact in int32.  e4m3: exact products, fp32 sums.  The RW * MT sums
+// steps, 16 bytes of every row a lane; the activation rows come from L1.  int8:
+// four-way integer dot products, exact in int32.  e4m3: exact products, fp32 sums.  The RW * MT sums
 // are added over the lanes by halving (each step trades half of the values for
 // the other half), so a value ends in 32 / (RW MT) lanes of its own; the order of
 // the additions is fixed.
