@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                 for (int kb = 0; kb < nkb && x_loads > 0 && good; ++kb)
                     mbar_wait(&x_full[kb], static_cast<uint32_t>(x_loads - 1) & 1u, lim);
         }
-        ok = good;
+        ok = __all_sync(0xffffffffu, good);
     } else if (warp == 1) {
         // ============================================================ MMA issue
         if (leader) {
@@ -620,10 +620,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
         if (__any_sync(0xffffffffu, (nf & 0x7FFF7FFFu) != 0) && lane == 0)
             atomicOr(&ctl->status, 1u << kStatusRange);
     }
-    if (SPLIT && warp < kEpiWarp0) {
-        __syncwarp();
-        cluster_wait();
-    }
+    if (SPLIT && warp < kEpiWarp0) cluster_wait();
     if (!ok) {
         atomicOr(&ctl->status, 1u << kStatusTimeout);
         if (SPLIT)
@@ -632,7 +629,6 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
                                            static_cast<uint32_t>(r)), 1);
     }
     tc_fence_before_sync();
-    if (SPLIT) __syncwarp();
     if (PAIR || SPLIT) cluster_sync();
     else __syncthreads();
     if (SPLIT && warp >= kEpiWarp0 && *failed == 0) {

@@ -99,8 +99,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 // Full cluster barrier (every thread of every CTA of the cluster), with
 // release/acquire ordering of shared-memory accesses across the cluster.
 // All CTAs of a cluster are resident together, so it completes once each
-// thread has reached it.  Warp-collective (.aligned): call it converged.
+// thread has reached it.  The .aligned forms want a warp's lanes together, and
+// callers come from loops that poll a barrier lane by lane, so each of these
+// gathers the warp first: all of its lanes call it.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile(
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -108,9 +111,11 @@ __device__ __forceinline__ void cluster_sync() {
 
 // The same barrier in two halves, with work of the caller's between them.
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
