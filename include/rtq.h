@@ -505,7 +505,7 @@ rt_status rt_dequant_e4m3_f16(const uint8_t *Wq, uint16_t *W_out, int64_t N, int
  *   fmt RT_FMT_Q8    int8 codes, scale = max|v| / 127, code = v / scale rounded
  *                    to nearest, ties to even: rt_quantize_q8_row's rule, and
  *                    for fp32 input its bits, so device-made codes are q8
- *                    weights too;
+ *                    weights too, for the next call on the stream already;
  *   fmt RT_FMT_E4M3  float8_e4m3fn codes, scale = max|v| / 448, code = the
  *                    e4m3 value nearest v / scale.
  * A row of zeros has scale 0 and zero codes.  A row in which a value is

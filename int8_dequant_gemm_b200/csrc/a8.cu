@@ -360,8 +360,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 1 ? 2 : 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     // Every operand, the weights and scales too, may be the previous kernel's
-    // output.  Dependents are released only after that kernel is complete, so
-    // one that reads ahead of its own wait reads nothing older than this grid.
+    // output.
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     bool ok = true;

@@ -259,10 +259,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     constexpr int V = Vec<T>::n;
     __shared__ float2 part[64];
     int turn = 0;
-    // X may be the previous kernel's output, and the outputs its input.  This
-    // kernel does not release its dependents early: its codes may be the
-    // weights of the next product, whose kernels read weights before they
-    // wait for this grid.
+    // X may be the previous kernel's output, and the outputs its input.  The
+    // codes may be the next product's weights: whatever reads weights before
+    // its own wait is launched by a pre-pass that has waited for this grid.
     pdl_wait_prior_grid();
     const int per_block = blockDim.x / TPR;
     const int t = threadIdx.x % TPR;

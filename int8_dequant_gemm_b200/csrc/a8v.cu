@@ -55,8 +55,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     using Acc = std::conditional_t<FMT == kFmtQ8, int, float>;
     constexpr int kVals = RW * MT;
     static_assert(kVals <= 32, "a value a lane");
-    // every operand may be the previous kernel's output; dependents are
-    // released after that kernel is complete
+    // every operand may be the previous kernel's output
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;

@@ -226,10 +226,11 @@ rt_status run_gemm(int fmt, const float *X, const void *Wq, const void *S, const
         return from_cuda(rtq::launch_xp(fmt, X, Wq, S, bias, Y, m, n, k, ctl, s));
     void *xh = nullptr;
     if ((st = workspace(s, static_cast<size_t>(M) * K * 2, &xh)) != RT_OK) return st;
-    cudaError_t e = rtq::launch_cvt_x16(X, xh, M, K, ctl, s);
+    const bool w_wait = kern == RT_KERNEL_TC_X_RESIDENT && rtq::xs_waits_for_weights(M, K);
+    cudaError_t e = rtq::launch_cvt_x16(X, xh, M, K, w_wait, ctl, s);
     if (e != cudaSuccess) return RT_ERR_CUDA;
     if (kern == RT_KERNEL_TC_X_RESIDENT)
-        return from_cuda(rtq::launch_xs(fmt, xh, Wq, S, bias, Y, m, n, k, ctl, s));
+        return from_cuda(rtq::launch_xs(fmt, xh, Wq, S, bias, Y, m, n, k, ctl, s, w_wait));
     return from_cuda(rtq::launch_ws(fmt, xh, Wq, S, bias, Y, m, n, k, ctl, s));
 }
 

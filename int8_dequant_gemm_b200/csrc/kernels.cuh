@@ -89,8 +89,10 @@ cudaError_t launch_tc_group(const GroupProblem *probs, int count, int M, DevCtl 
 // which fits beside a CTA of the activation-resident kernel, for an input
 // rounded on a second stream while that kernel runs (no programmatic
 // dependent launch).
-cudaError_t launch_cvt_x16(const float *X, void *Xh, int64_t M, int64_t K, DevCtl *ctl,
-                           cudaStream_t s);
+// launch_cvt_x16's next_waits: the launch behind it reads nothing before its
+// own dependency wait (launch_xs with w_wait) and may start with this one.
+cudaError_t launch_cvt_x16(const float *X, void *Xh, int64_t M, int64_t K, bool next_waits,
+                           DevCtl *ctl, cudaStream_t s);
 cudaError_t launch_cvt_x16_lean(const float *X, void *Xh, int64_t M, int64_t K, DevCtl *ctl,
                                 cudaStream_t s);
 // The lean pre-pass's block: threads and registers a thread; false if the
@@ -120,8 +122,18 @@ bool xs_group_supported(const XsInput *in, int count, int M);
 // this list (per sub-partition registers, shared memory, threads).
 bool xs_group_leaves_room(const XsInput *in, int count, int M, int threads, int regs);
 cudaError_t launch_xs(int fmt, const void *Xh, const void *Wq, const void *S, const float *bias,
-                      float *Y, int M, int N, int K, DevCtl *ctl, cudaStream_t s);
-cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cudaStream_t s);
+                      float *Y, int M, int N, int K, DevCtl *ctl, cudaStream_t s,
+                      bool w_wait = false);
+cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cudaStream_t s,
+                            bool w_wait = false);
+// Weights may be the output of the launch before the call, so they are read
+// after a wait for it: the pre-pass's, which then lets this kernel start, or
+// (w_wait) this kernel's own, with the start together with the pre-pass.  The
+// second where the pre-pass is shorter than a launch.  us a call, back to back,
+// first and second: 129 x 512 x 512 8.6 and 7.6, 300 x 4096 x 512 9.0 and 8.1,
+// 1000 x 2048 x 512 9.2 and 8.9, 2048 x 4096 x 512 16.5 and 16.4, 4096 x 4096 x
+// 512 26.6 and 26.5 (reading them after neither, 7.1, 7.6, 8.2, 16.4, 26.5).
+inline bool xs_waits_for_weights(int64_t M, int64_t K) { return M * K < (int64_t(1) << 20); }
 
 // The same activation-resident product on CTA pairs (cta_group::2, 256 weight
 // rows per MMA), rounding fp32 X to fp16 inside the kernel; see xp.cu.  Same

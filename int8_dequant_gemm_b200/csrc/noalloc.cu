@@ -76,8 +76,9 @@ extern "C" rt_status rt_qgemm_noalloc(int fmt, const float *X, const void *Wq, c
         return from_cuda(rtq::launch_tc(fmt, X, Wq, scales, nullptr, Y, m, n, k, ctl, s));
     if (kern == RT_KERNEL_TC_X_RESIDENT_PAIR)
         return from_cuda(rtq::launch_xp(fmt, X, Wq, scales, nullptr, Y, m, n, k, ctl, s));
-    if (rtq::launch_cvt_x16(X, xh, M, K, ctl, s) != cudaSuccess) return RT_ERR_CUDA;
+    const bool w_wait = kern == RT_KERNEL_TC_X_RESIDENT && rtq::xs_waits_for_weights(M, K);
+    if (rtq::launch_cvt_x16(X, xh, M, K, w_wait, ctl, s) != cudaSuccess) return RT_ERR_CUDA;
     if (kern == RT_KERNEL_TC_X_RESIDENT)
-        return from_cuda(rtq::launch_xs(fmt, xh, Wq, scales, nullptr, Y, m, n, k, ctl, s));
+        return from_cuda(rtq::launch_xs(fmt, xh, Wq, scales, nullptr, Y, m, n, k, ctl, s, w_wait));
     return from_cuda(rtq::launch_ws(fmt, xh, Wq, scales, nullptr, Y, m, n, k, ctl, s));
 }

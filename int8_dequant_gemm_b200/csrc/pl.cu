@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kPlThreads, 1)
 
     if (warp == kProdWarp) {
         // ======================================================= weight producer
-        // Packed weights do not depend on the previous kernel in the stream.
+        // Packed weights do not depend on the previous kernel in the stream, the
+        // pre-pass or a list launch, and what came before that is complete.
         // (Test hook: with `inject`, the first slot is never loaded, so the
         // dequantizers' wait for it runs out.)
         if (lane == 0) {
@@ -672,11 +673,11 @@ __global__ void __launch_bounds__(kPlThreads, 1)
 // not a finite fp16 value after rounding latches kStatusRange.
 __global__ void __launch_bounds__(256)
     pl_prep_kernel(const __grid_constant__ PlPrep P, DevCtl *ctl) {
-    // The list launch that follows may start right away: its weight copies
-    // do not depend on this kernel, and it reads the images only after its
-    // own wait for this grid's completion.
-    pdl_launch_dependents();
+    // The list launch that follows may start once the launches before this
+    // one are complete: its weights, which one of them may have written, it
+    // reads at once, and the images after its own wait for this grid.
     pdl_wait_prior_grid();
+    pdl_launch_dependents();
     const PlPrepImage &im = P.img[blockIdx.y];
     const int BNp = P.bnp, M = P.M, K = im.K;
     const int64_t pieces = static_cast<int64_t>(K / 8) * BNp;   // 16-byte output pieces

@@ -20,11 +20,14 @@ namespace {
 
 __global__ void __launch_bounds__(256)
     cvt_x16_kernel(const float4 *__restrict__ X, uint4 *__restrict__ Xh, int64_t n_chunks,
-                   DevCtl *ctl) {
-    // the next kernel may be scheduled now: it reads this one's output only
-    // after its own wait for this grid's completion
-    pdl_launch_dependents();
+                   int next_waits, DevCtl *ctl) {
+    // The next kernel, a GEMM, may be scheduled once the launches before this
+    // one are complete: it reads its weights, which one of them may have
+    // written, at once, and this grid's output after its own wait for it.
+    // next_waits: it waits before it reads anything, and may be scheduled now.
+    if (next_waits) pdl_launch_dependents();
     pdl_wait_prior_grid();
+    pdl_launch_dependents();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     uint32_t bad = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n_chunks;
@@ -91,8 +94,8 @@ struct CvtGroup {
 
 __global__ void __launch_bounds__(256) cvt_x16_group_kernel(const __grid_constant__ CvtGroup g,
                                                             DevCtl *ctl) {
+    pdl_wait_prior_grid();     // as in cvt_x16_kernel
     pdl_launch_dependents();
-    pdl_wait_prior_grid();
     const int64_t total = g.end[g.count - 1];
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     uint32_t bad = 0;
@@ -130,14 +133,15 @@ cudaLaunchConfig_t cvt_config(int64_t n_chunks, cudaStream_t s, cudaLaunchAttrib
 
 }  // namespace
 
-cudaError_t launch_cvt_x16(const float *X, void *Xh, int64_t M, int64_t K, DevCtl *ctl,
-                           cudaStream_t s) {
+cudaError_t launch_cvt_x16(const float *X, void *Xh, int64_t M, int64_t K, bool next_waits,
+                           DevCtl *ctl, cudaStream_t s) {
     const int64_t n_chunks = M * K / 8;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = cvt_config(n_chunks, s, attr);
     const float4 *x4 = reinterpret_cast<const float4 *>(X);
     uint4 *h = static_cast<uint4 *>(Xh);
-    return cudaLaunchKernelEx(&cfg, cvt_x16_kernel, x4, h, n_chunks, ctl);
+    return cudaLaunchKernelEx(&cfg, cvt_x16_kernel, x4, h, n_chunks, next_waits ? 1 : 0,
+                              ctl);
 }
 
 cudaError_t launch_cvt_x16_lean(const float *X, void *Xh, int64_t M, int64_t K, DevCtl *ctl,

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(kWsThreads, 1)
 
     if (warp == kWTmaWarp) {
         // ============================================================ weight TMA
+        // (before the dependency wait, as in xs.cu; with x_ready the call's
+        // earlier launches began with a pre-pass)
         // (Test hook: with `inject` the first packed-code box is never
         // requested, so the dequantizers' wait for it runs out.)
         if (lane == 0) {

@@ -265,6 +265,9 @@ __global__ void __launch_bounds__(kXpThreads, 1)
     cluster_sync();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    // No pre-pass stands before this launch: X, and the weights too, may be the
+    // previous kernel's output.
+    pdl_wait_prior_grid();
     // The next kernel in the stream may be scheduled from here on: whatever it
     // reads of this one's output it reads after its own wait for this grid's
     // completion, and its CTAs take SMs only as this grid's leave them.
@@ -323,7 +326,6 @@ __global__ void __launch_bounds__(kXpThreads, 1)
         // fp32 values (this CTA's half of the block), in atom order, through
         // the staging ring; rows past M read as zero.
         if (lane == 0) {
-            pdl_wait_prior_grid();     // X may be the output of the previous kernel
             int cur_m = -1, j = 0;
             for (ItemCursor it(first, last, n_op); it.valid() && ok; it.next()) {
                 if (it.m_tile == cur_m) continue;

@@ -145,6 +145,7 @@ struct XsProblem {
 struct XsParams {
     XsProblem p[kMaxGroup];
     int count, M, n_m, n_items;
+    int w_wait;                      // the weights are read after the dependency wait too
 };
 
 // Iterates a CTA's run of (problem, activation block, weight tile) items
@@ -287,11 +288,14 @@ __global__ void __maxnreg__(kXsMaxRegs)
 
     if (warp == kWTmaWarp) {
         // ============================================================ weight TMA
-        // Packed weights do not depend on the previous kernel in the stream,
-        // so this role starts before the dependency wait.  (Test hook: with
+        // Packed weights do not depend on the previous kernel in the stream, the
+        // pre-pass, and what came before that is complete (the pre-pass lets
+        // this launch start after its own wait), so this role starts before
+        // the dependency wait, unless w_wait.  (Test hook: with
         // `inject` the first packed-code box is never requested, so the
         // dequantizers' wait for it runs out.)
         if (lane == 0) {
+            if (P.w_wait) pdl_wait_prior_grid();
             int j = 0, n_sc = 0;
             for (ItemCursor it(P, first, last); it.valid() && ok; it.next(P)) {
                 const XsProblem &q = P.p[it.pi];
@@ -712,7 +716,8 @@ bool xs_group_leaves_room(const XsInput *in, int count, int M, int threads, int 
     return per_sub <= sm_regs / 4 && smem <= sm_smem && kXsThreads + threads <= sm_threads;
 }
 
-cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cudaStream_t s) {
+cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cudaStream_t s,
+                            bool w_wait) {
     if (!xs_group_supported(in, count, M)) return cudaErrorInvalidValue;
     bool mixed = false;
     int k_max = 0;
@@ -724,6 +729,7 @@ cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cu
     XsParams P = {};
     P.count = count;
     P.M = M;
+    P.w_wait = w_wait ? 1 : 0;
     P.n_m = (M + kXsTileM - 1) / kXsTileM;
     int items = 0;
     for (int i = 0; i < count; ++i) {
@@ -739,9 +745,9 @@ cudaError_t launch_xs_group(const XsInput *in, int count, int M, DevCtl *ctl, cu
 }
 
 cudaError_t launch_xs(int fmt, const void *Xh, const void *Wq, const void *S, const float *bias,
-                      float *Y, int M, int N, int K, DevCtl *ctl, cudaStream_t s) {
+                      float *Y, int M, int N, int K, DevCtl *ctl, cudaStream_t s, bool w_wait) {
     const XsInput in = {fmt, Xh, Wq, S, bias, Y, N, K};
-    return launch_xs_group(&in, 1, M, ctl, s);
+    return launch_xs_group(&in, 1, M, ctl, s, w_wait);
 }
 
 }  // namespace rtq
