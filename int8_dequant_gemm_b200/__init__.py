@@ -328,6 +328,19 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream):
+    """An output that the caller did not bring, from the memory of the stream
+    that the call runs on: a block of another stream's may still be in that
+    one's use, or be given out again by it, while the call writes it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t, dtype, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -393,7 +406,7 @@ def qgemm_q4(X, Wq, scale_min, Y=None, path="auto", stream=None):
     import torch
     M, N, K = _check_gemm_shapes(4, X, Wq, scale_min, Y)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _new((M, N), torch.float32, X.device, stream)
     st = rt_qgemm_q4(_dev(X, torch.float32, "X"), _dev(Wq, torch.uint8, "Wq"),
                      _dev(scale_min, torch.uint16, "scale_min"), _dev(Y, torch.float32, "Y"),
                      M, N, K, _path(path), _stream_ptr(stream))
@@ -406,7 +419,7 @@ def qgemm_q8(X, Wq, scale, Y=None, path="auto", stream=None):
     import torch
     M, N, K = _check_gemm_shapes(8, X, Wq, scale, Y)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _new((M, N), torch.float32, X.device, stream)
     st = rt_qgemm_q8(_dev(X, torch.float32, "X"), _dev(Wq, torch.int8, "Wq"),
                      _dev(scale, torch.float32, "scale"), _dev(Y, torch.float32, "Y"),
                      M, N, K, _path(path), _stream_ptr(stream))
@@ -420,7 +433,7 @@ def qgemm(fmt, X, Wq, scales=None, bias=None, Y=None, path="auto", stream=None):
     import torch
     M, N, K = _check_gemm_shapes(fmt, X, Wq, scales, Y)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _new((M, N), torch.float32, X.device, stream)
     b = None
     if bias is not None:
         _shape(bias, (N,), "bias")
@@ -437,7 +450,7 @@ def gemm_e4m3(X, W, Y=None, path="auto", stream=None):
     import torch
     M, N, K = _check_gemm_shapes(FMT_E4M3, X, W, None, Y)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _new((M, N), torch.float32, X.device, stream)
     st = rt_gemm_e4m3(_dev(X, torch.float32, "X"), _dev(W, torch.uint8, "W"),
                       _dev(Y, torch.float32, "Y"), M, N, K, _path(path), _stream_ptr(stream))
     _check(st, "rt_gemm_e4m3")
@@ -462,7 +475,9 @@ def qgemm_noalloc(fmt, X, Wq, scales, Y, path="auto", stream=None):
 # ---------------------------------------------------------- 8-bit activations
 # These calls run a few microseconds on the GPU, so what the helpers do before
 # the launch counts: each checks all its operands in one expression (about 0.25
-# us an operand), and only when that fails looks for what to say.
+# us an operand), and only when that fails looks for what to say.  With `stream`,
+# outputs that are not given come from that stream's memory; keeping the inputs'
+# memory until the stream has read them is the caller's, as in torch.
 _a8_state = None
 
 
@@ -542,9 +557,9 @@ def _a8_stream(stream, index, state):
     return stream.cuda_stream
 
 
-def _a8_new(shape, dtype, index):
+def _a8_new(shape, dtype, index, stream):
     import torch
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    return _new(shape, dtype, torch.device("cuda", index), stream)
 
 
 def quantize_a8(X, fmt=FMT_Q8, codes=None, scales=None, stream=None):
@@ -553,9 +568,9 @@ def quantize_a8(X, fmt=FMT_Q8, codes=None, scales=None, stream=None):
     state, cdt, dt, M, K, index = _a8_open(fmt, X, "X")
     f32 = state[2]
     if codes is None:
-        codes = _a8_new((M, K), cdt, index)
+        codes = _a8_new((M, K), cdt, index, stream)
     if scales is None:
-        scales = _a8_new((M,), f32, index)
+        scales = _a8_new((M,), f32, index, stream)
     if not (X.is_contiguous() and _a8_fits(codes, cdt, (M, K), index) and
             _a8_fits(scales, f32, (M,), index)):
         _a8_refuse(index, (X, X.dtype, (M, K), "X"), (codes, cdt, (M, K), "codes"),
@@ -576,11 +591,11 @@ def addnorm_a8(X, gain=None, fmt=FMT_Q8, residual=None, eps=1e-6, H=None, codes=
     state, cdt, dt, M, K, index = _a8_open(fmt, X, "X")
     f32, xdt, shape = state[2], X.dtype, (M, K)
     if residual is not None and H is None:
-        H = _a8_new(shape, xdt, index)
+        H = _a8_new(shape, xdt, index, stream)
     if codes is None:
-        codes = _a8_new(shape, cdt, index)
+        codes = _a8_new(shape, cdt, index, stream)
     if scales is None:
-        scales = _a8_new((M,), f32, index)
+        scales = _a8_new((M,), f32, index, stream)
     if not (X.is_contiguous() and (residual is None or _a8_fits(residual, xdt, shape, index)) and
             (gain is None or _a8_fits(gain, f32, (K,), index)) and
             (H is None or _a8_fits(H, xdt, shape, index)) and _a8_fits(codes, cdt, shape, index) and
@@ -607,9 +622,9 @@ def gate_a8(U, fmt=FMT_Q8, codes=None, scales=None, stream=None):
     if F2 % 2:
         raise ValueError(f"U must hold two halves, got {F2} columns")
     if codes is None:
-        codes = _a8_new((M, F), cdt, index)
+        codes = _a8_new((M, F), cdt, index, stream)
     if scales is None:
-        scales = _a8_new((M,), f32, index)
+        scales = _a8_new((M,), f32, index, stream)
     if not (U.is_contiguous() and _a8_fits(codes, cdt, (M, F), index) and
             _a8_fits(scales, f32, (M,), index)):
         _a8_refuse(index, (U, U.dtype, (M, F2), "U"), (codes, cdt, (M, F), "codes"),
@@ -626,7 +641,7 @@ def dequant_a8(fmt, codes, scales, dtype=None, out=None, stream=None):
     state, cdt, _, M, K, index = _a8_open(fmt, codes, "codes", True)
     if out is None:
         import torch
-        out = _a8_new((M, K), dtype or torch.bfloat16, index)
+        out = _a8_new((M, K), dtype or torch.bfloat16, index, stream)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype {dtype}")
     dt = _a8_open(fmt, out, "out")[2]
@@ -655,7 +670,7 @@ def qgemm_a8(fmt, Xq, x_scales, Wq, w_scales=None, bias=None, Y=None, dtype=None
     if fmt == FMT_Q8 and w_scales is None:
         raise TypeError("q8 weights have row scales")
     if Y is None:
-        Y = _a8_new((M, N), dtype or f32, index)
+        Y = _a8_new((M, N), dtype or f32, index, stream)
     elif dtype is not None and Y.dtype != dtype:
         raise TypeError(f"Y is {Y.dtype}, dtype {dtype}")
     ydt = getattr(Y, "dtype", None)
@@ -887,7 +902,7 @@ def quantize_e4m3(W: np.ndarray) -> np.ndarray:
 def dequant_e4m3_f32(Wq, stream=None):
     import torch
     N, K = Wq.shape
-    out = torch.empty((N, K), dtype=torch.float32, device=Wq.device)
+    out = _new((N, K), torch.float32, Wq.device, stream)
     _check(rt_dequant_e4m3_f32(_dev(Wq, torch.uint8, "Wq"), _dev(out, torch.float32, "W_out"),
                                N, K, _stream_ptr(stream)), "rt_dequant_e4m3_f32")
     return out
@@ -897,7 +912,7 @@ def dequant_e4m3_f16(Wq, stream=None):
     """The tensor-core operand of e4m3 weights, as fp16 bits (uint16) [N, K]."""
     import torch
     N, K = Wq.shape
-    out = torch.empty((N, K), dtype=torch.uint16, device=Wq.device)
+    out = _new((N, K), torch.uint16, Wq.device, stream)
     _check(rt_dequant_e4m3_f16(_dev(Wq, torch.uint8, "Wq"), _dev(out, torch.uint16, "W_out"),
                                N, K, _stream_ptr(stream)), "rt_dequant_e4m3_f16")
     return out
@@ -918,7 +933,7 @@ def dequant_q4_f32(Wq, scale_min, stream=None):
     import torch
     N, K2 = Wq.shape
     _shape(scale_min, _packed_shapes(4, N, 2 * K2)[1], "scale_min")
-    out = torch.empty((N, 2 * K2), dtype=torch.float32, device=Wq.device)
+    out = _new((N, 2 * K2), torch.float32, Wq.device, stream)
     st = rt_dequant_q4_f32(_dev(Wq, torch.uint8, "Wq"), _dev(scale_min, torch.uint16, "scale_min"),
                            _dev(out, torch.float32, "W_out"), N, 2 * K2, _stream_ptr(stream))
     _check(st, "rt_dequant_q4_f32")
@@ -930,7 +945,7 @@ def dequant_q4_f16(Wq, scale_min, stream=None):
     import torch
     N, K2 = Wq.shape
     _shape(scale_min, _packed_shapes(4, N, 2 * K2)[1], "scale_min")
-    out = torch.empty((N, 2 * K2), dtype=torch.uint16, device=Wq.device)
+    out = _new((N, 2 * K2), torch.uint16, Wq.device, stream)
     st = rt_dequant_q4_f16(_dev(Wq, torch.uint8, "Wq"), _dev(scale_min, torch.uint16, "scale_min"),
                            _dev(out, torch.uint16, "W_out"), N, 2 * K2, _stream_ptr(stream))
     _check(st, "rt_dequant_q4_f16")
@@ -941,7 +956,7 @@ def dequant_q8_f32(Wq, scale, stream=None):
     import torch
     N, K = Wq.shape
     _shape(scale, (N,), "scale")
-    out = torch.empty((N, K), dtype=torch.float32, device=Wq.device)
+    out = _new((N, K), torch.float32, Wq.device, stream)
     st = rt_dequant_q8_f32(_dev(Wq, torch.int8, "Wq"), _dev(scale, torch.float32, "scale"),
                            _dev(out, torch.float32, "W_out"), N, K, _stream_ptr(stream))
     _check(st, "rt_dequant_q8_f32")

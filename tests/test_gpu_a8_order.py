@@ -128,3 +128,29 @@ def test_8bit_product(rtq, busy, M, fmt):
     x = rtq.quantize_a8(randn(M, K, seed=90), fmt)
     turns(rtq, fmt, N, K, lambda c, s: rtq.qgemm_a8(fmt, *x, c, s), busy,
           lambda c, s: rtq.qgemm_a8(fmt, *x, c, s))
+
+
+def test_outputs_a_helper_allocates_on_another_stream(rtq, busy):
+    """Blocks that work pending on the current stream still uses are not given to a
+    call on another one, and its results are the current stream's."""
+    M, K, N = 700, 512, 300
+    x, r = randn(M, K, seed=1), randn(M, K, seed=2)
+    w = rtq.quantize_a8(randn(N, K, seed=3), Q8)
+    want = [*rtq.quantize_a8(x, Q8), *rtq.addnorm_a8(x, None, Q8, residual=r), *rtq.gate_a8(x, Q8)]
+    want += [rtq.dequant_a8(Q8, *want[:2]), rtq.qgemm_a8(Q8, *want[:2], *w), rtq.qgemm_q8(x, *w)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks of every output's size, used by work behind `busy` and then free
+    busy()
+    held = [torch.full_like(t, 5) for t in want]
+    kept = [t + 0 for t in held]
+    blocks = {t.data_ptr() for t in held}
+    del held
+    got = [*rtq.quantize_a8(x, Q8, stream=side), *rtq.addnorm_a8(x, None, Q8, residual=r, stream=side),
+           *rtq.gate_a8(x, Q8, stream=side)]
+    got += [rtq.dequant_a8(Q8, *got[:2], stream=side), rtq.qgemm_a8(Q8, *got[:2], *w, stream=side),
+            rtq.qgemm_q8(x, *w, stream=side)]
+    assert not blocks & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    for a, b, k in zip(want, got, kept):
+        assert torch.equal(a, b) and bool((k == 5).all())
