@@ -555,6 +555,8 @@ rt_status rt_addnorm_a8(int fmt, int dtype, const void *X, const void *R, const 
 /*
  * Gated SiLU into 8 bits: U [M, 2F] holds a | b (the rows a w1|w3 projection
  * gives), y = a * sigmoid(a) * b, codes [M, F], scales [M] = y in 8 bits.
+ * sigmoid(a) below 2^-126 (a < -87.3) counts as 0; elsewhere y is off by about
+ * as many roundings as a / (1 + expf(-a)) * b in fp32.
  */
 rt_status rt_gate_a8(int fmt, int dtype, const void *U, void *codes, float *scales, int64_t M,
                      int64_t F, void *stream);
