@@ -1,5 +1,6 @@
 """How many roundings the row operators take, in units of u = 2^-24 (half an ulp of
 fp32 at most): bounds counted operation by operation, before their first run."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -95,3 +96,24 @@ def test_gate_of_the_smallest_sigmoids(rtq, fmt):
     y = (x * torch.sigmoid(x) * u[:3, 18].double()).abs()
     assert float(((s[:3].double() * TOP[fmt] - y).abs() / y / U - 0.05 * x.abs()).max()) <= 11
     assert bool((s[3:] == 0).all()) and bool((c[3:].to(torch.int32) == 0).all())
+
+
+@pytest.mark.parametrize("K", [16, 80, 208, 512, 528, 1040, 2048, 4112])
+def test_norm_roundings(rtq, K):
+    """Rows of small integers, whose maximum and sum of squares are exact.  The
+    formula's own steps in fp32, rounded once each: the quotient by K and the sum with
+    eps (halved by the root), the root, the maximum over 127 and the product, 1 + 1 +
+    1 + 1 = 4 u.  The kernel's rounded 1 / K and approximate root are to add nothing
+    to that."""
+    M, eps = 1 << 15, float(np.float32(1e-5))
+    g = torch.Generator(device="cuda").manual_seed(K)
+    top = torch.randint(1, 16, (M, 1), generator=g, device="cuda")
+    x = torch.randint(-15, 16, (M, K), generator=g, device="cuda").clamp(-top, top)
+    x[:, 0] = top[:, 0]
+    _, s, _ = rtq.addnorm_a8(x.float(), None, Q8, eps=eps)
+    h = x.double()
+    ss = h.square().sum(1)
+    assert float(ss.max()) < 2 ** 24
+    want = h.abs().amax(1) / TOP[Q8] / torch.sqrt(ss / K + eps)
+    err = float(((s.double() - want).abs() / want).max() / U)
+    assert err <= 4, err
