@@ -764,24 +764,40 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
 
 // Pairs: an activation tile stays in shared memory for all weight tiles (RES), which
 // takes half of the operand bytes off the way from L2, where the other operand's ring
-// keeps enough stages and the weights stay in L2.  Rows that are no multiple of 128
-// bytes gain most: a piece of them lies across two L2 lines.  us, streamed and
-// kept, bf16: 20001 x 2003 x 1040 55.6 and 49.6, 32768 x 2048 x 400 43.7 and 38.8,
-// 65536 x 4096 x 512 150 and 143, 16384 x 4096 x 768 46.8 and 45.0; 20001 x 2048 x
-// 1024 35.7 and 37.8 (four stages left); fp32: 16384 x 2048 x 528 33.7 and 30.9, 16384 x 4096 x 768 65.0
-// and 60.6; 32768 x 2048 x 512 52.6 and 57.9 (bound by the stores of Y, which follow
-// each other more closely in bands); bf16 65536 x 512 x 512 21.8 and 22.5 (two tiles).
-bool activations_stay(int N, int K, size_t y_bytes) {
+// keeps enough stages, the weights stay in L2 and there is more than one weight
+// tile.  It gains most where rows of K lie across L2 lines, a piece over two; it
+// loses where rows of Y begin inside a 32-byte sector and Y is larger than L2, unless
+// K is long: its walk leaves the sectors at its tiles' edges half written for
+// longer.  Time kept over time streamed, means of 2200 timings (M 12000 to 65536, N
+// 300 to 8192):
+//   K not a multiple of 64, by pieces of 128   2     3     4     5     7     8
+//     rows of Y whole, bf16, Y from 128 MB on 0.95  0.91  0.85  0.82  0.80  0.80
+//     the same, fp32                          1.04  0.99  0.94  0.90  0.87  0.89
+//     ragged, bf16                            1.26  1.21  1.10  0.99  0.86  0.82
+//     ragged, fp32                            1.07  1.16  1.21  1.13  0.98  0.88
+//     Y within 128 MB, all four          0.95-1.12  0.88-1.07  0.88-1.00  0.88-0.98  ...
+//   K an odd multiple of 64, 6 and 8 pieces: bf16 0.94 to 1.07, fp32 0.90 to 1.03 (ragged
+//     and large 1.22 and 1.05); 3 pieces 1.0 to 1.3, 9 0.9 to 1.1
+//   K a multiple of 128: 1.0 to 1.3, but for whole rows of N >= 4096, bf16 up to 6
+//     pieces 0.93 to 1.01, fp32 6 pieces 0.90 to 0.96
+// One weight tile: 0.99 to 1.06 bf16, 0.90 to 1.03 fp32.
+bool activations_stay(int M, int N, int K, size_t y_bytes) {
     const int nkb = (K + kKBytes - 1) / kKBytes;
-    if (nkb > kResAtoms || static_cast<int64_t>(N) * K > (int64_t(32) << 20)) return false;
-    return K % kKBytes != 0 || (N >= 1024 && nkb <= 6 && (y_bytes == 2 || nkb > 4));
+    if (nkb > kResAtoms || static_cast<int64_t>(N) * K > (int64_t(32) << 20) || N <= 2 * kTileRows)
+        return false;
+    const bool half = y_bytes == 2, whole = N * y_bytes % 32 == 0;
+    const bool large = M * (N * y_bytes) >= (size_t(128) << 20);
+    if (K % 128 == 0) return whole && N >= 4096 && nkb <= 6 && (half || nkb == 6);
+    if (K % 64 == 0) return nkb >= 6 && nkb <= 8 && (whole || half || !large);
+    if (large && whole && half) return nkb >= 2;
+    return nkb >= (large && !whole ? (half ? 5 : 8) : 4);
 }
 
 template <int FMT, typename YT>
 cudaError_t launch_a8_p(const A8Plan &p, const void *Xq, const float *xs, const void *Wq,
                         const float *wsc, const float *bias, void *Y, int M, int N, int K,
                         DevCtl *ctl, cudaStream_t s) {
-    if (p.pair && activations_stay(N, K, sizeof(YT)))
+    if (p.pair && activations_stay(M, N, K, sizeof(YT)))
         return launch_a8<FMT, YT, true, 4, false, true>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);
     if (p.pair)
         return launch_a8<FMT, YT, true, 4, false, false>(p, Xq, xs, Wq, wsc, bias, Y, M, N, K, ctl, s);

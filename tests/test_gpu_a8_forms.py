@@ -115,8 +115,8 @@ def test_shared_k(rtq, fmt, M, N, K, rows, split):
 
 
 # CTA pairs: one tile each, and walks with the activations kept and streamed
-PAIRS = [(256, 8192, 8192, False), (512, 4096, 8192, False), (9001, 2003, 640, True), (9000, 2050, 1280, False),
-         (7003, 4100, 1040, True)]
+PAIRS = [(256, 8192, 8192, False), (512, 4096, 8192, False), (9001, 2003, 640, False), (9000, 2050, 1280, False),
+         (7003, 4100, 1040, True), (9000, 4096, 640, True), (9001, 2003, 592, True), (20000, 250, 1040, False)]
 
 
 @pytest.mark.parametrize("M,N,K,kept", PAIRS)
@@ -126,6 +126,16 @@ def test_pairs(rtq, fmt, M, N, K, kept):
     assert p["pair"] and p["walk"]
     check_product(rtq, fmt, M, N, K, seed=M + N)
     runs_as(rtq, fmt, M, N, K, torch.bfloat16, f"true, 4, false, {str(kept).lower()}>")
+
+
+@pytest.mark.parametrize("M,N,K,dtype,kept", [
+    (65536, 2003, 400, torch.float32, False), (65536, 2003, 400, torch.bfloat16, False),   # ragged rows of Y
+    (65536, 2003, 1040, torch.bfloat16, True), (65536, 2048, 400, torch.bfloat16, True),
+    (65536, 2003, 512, torch.bfloat16, False), (65536, 4096, 512, torch.bfloat16, True),
+    (65536, 4096, 512, torch.float32, False), (65536, 200, 272, torch.float32, False)])    # one weight tile
+def test_activations_are_kept_where_that_is_faster(rtq, M, N, K, dtype, kept):
+    assert rtq.a8_plan(M, N, K)["pair"]
+    runs_as(rtq, Q8, M, N, K, dtype, f"true, 4, false, {str(kept).lower()}>")
 
 
 # one form each: name, M, N, K
