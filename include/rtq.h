@@ -507,7 +507,8 @@ rt_status rt_dequant_e4m3_f16(const uint8_t *Wq, uint16_t *W_out, int64_t N, int
  *                    for fp32 input its bits, so device-made codes are q8
  *                    weights too, for the next call on the stream already;
  *   fmt RT_FMT_E4M3  float8_e4m3fn codes, scale = max|v| / 448, code = the
- *                    e4m3 value nearest v / scale.
+ *                    e4m3 value nearest 448 v / max|v| (v / scale in rows
+ *                    whose max|v| is below 2^-100).
  * A row of zeros has scale 0 and zero codes.  A row in which a value is
  * infinite or NaN has scale NaN and zero codes, so the product makes that row
  * of Y NaN and leaves the others alone; it latches RT_ERR_OPERAND_RANGE for
@@ -520,7 +521,7 @@ rt_status rt_dequant_e4m3_f16(const uint8_t *Wq, uint16_t *W_out, int64_t N, int
  *   - all tensors are row-major and contiguous; K (F) is a multiple of 16 and
  *     at most 32768 for the calls that make 8-bit rows, 131056 for the product
  *     and rt_dequant_a8 (RT_ERR_UNSUPPORTED_SHAPE): a row stays in one
- *     block's registers, and the int8 product's sum in int32;
+ *     block, and the int8 product's sum in int32;
  *   - X, R, H, U, out, codes, Xq, Wq, Y and gain 16-byte aligned, scales and
  *     bias 4-byte aligned (RT_ERR_ALIGNMENT);
  *   - 0 <= M, 1 <= N, both below 2^31 - 1023; M == 0 is a no-op;

@@ -17,8 +17,13 @@
 // of the store instructions; 276 against 204 us for 65536 x 4096 x 512 into
 // fp32, 181 against 175 into bf16, then), and tiles of Y staged in shared memory
 // and stored by TMA (19.8 against 17.5 us for 4096 x 4096 x 512).
-// What bounds large products is bytes between L2 and the SMs, 10 to 12 TB/s of operands
-// and Y together (65536 x 4096 x 512: bf16 143 us, fp32 205; 8192^3 365).
+// What bounds large products: 8192^3 the tensor cores (94 % of their cycles at 4096 x
+// 8192 x 8192; 365 us); fp32 results of short K the bytes between L2 and the SMs,
+// operands and Y together 10 TB/s, L1 82 % busy (65536 x 4096 x 512 205 us).  16-bit results
+// move a third fewer with activations that stay (143 us, 7 TB/s): no unit is above 57 %
+// (issue slots, L1; tensor cores 44), so it is the latency of the epilogue's steps; the
+// same for ragged ones (20001 x 2003 x 1040 50 to 53 us, 7 TB/s, L1 64 %, issue slots 35 %,
+// with two stores for one).
 //
 // Roles (20 warps): warp 0 TMA, warp 1 MMA issue, warps 4-19 epilogue (four per
 // TMEM lane quadrant); warps 2-3 idle.
@@ -52,9 +57,10 @@ constexpr int kABytes = kTileRows * kKBytes;       // 16 KB of weights an atom
 // 12.3 -> 10.4; 8192^3 on pairs 369 -> 381).
 constexpr int stage_atoms(int pair) { return pair ? 1 : 2; }
 // Epilogue groups G of four warps, one per TMEM lane quadrant: 4 for persistent
-// tiles, 1 where a CTA has one narrow tile (192 threads and, but for the widest
-// splits, at most half an SM's registers and shared memory, so the next kernel's CTA
-// starts beside it).
+// tiles, 1 where a CTA has one narrow tile: 192 threads, at most half an SM's
+// registers and, up to 80 rows (32 with a split), half its shared memory, so that the next
+// kernel's CTA starts beside it.  Wider tiles need more for their two stages and the
+// split's partial sums, 119 to 199 KB.
 constexpr int epi_warp0(int G) { return G == 1 ? 2 : 4; }
 constexpr int cta_threads(int G) { return (epi_warp0(G) + 4 * G) * 32; }
 constexpr int kMaxStages = 8;
@@ -844,9 +850,9 @@ int sm_count() {
 // multiple of 128 bytes lie across two L2 lines a piece and count 1.5 times (20001 x
 // 2048 x 1040 bf16 47 us, K = 1024 36).  Weights of more than 60 MB come from HBM,
 // faster the more CTAs ask for them (16 x 8192 x 8192 on 64, 128 and 256 CTAs: 22, 16
-// and 14.7 us).  Fitted to 1.9 thousand timings; against every plan at M = 1 to 4096,
-// twelve weight shapes from 512 x 64 to 8192 x 8192 and both formats the one taken is on
-// average 1 % slower than the best, at most 20 %.
+// and 14.7 us).  The constants are a fit to timings of every plan at M = 1 to
+// 4096 and twelve weight shapes from 512 x 64 to 8192 x 8192, on the kernels of then; the
+// plan taken was on average 1 % slower than the best of a shape, at most 20 %.
 A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
     const int nkb = (K + kKBytes - 1) / kKBytes;
     const int n_o = static_cast<int>((static_cast<int64_t>(N) + kTileRows - 1) / kTileRows);
@@ -900,8 +906,14 @@ A8Plan plan_a8(int fmt, int M, int N, int K, int sms) {
         }
     // A few rows on the CUDA cores, 1 or 4 weight rows a warp (us beyond 1.76): a
     // 512-byte step of K costs a load's latency, a byte of weights its load or its
-    // arithmetic, in whole steps.  One weight row a warp where four would leave SMs without
-    // warps, or where the loads are the time.  Measured, us, CUDA cores and tensor
+    // arithmetic, in whole steps.  Up to four activation rows: one weight row a warp, whose
+    // loads of K all run at once, but four where K is short (below 1024) and there are enough
+    // weight rows (above 2048) to fill the SMs with a quarter of the warps.  One over
+    // four, int8, M = 1: 2048 x 512 0.94, 4096 x 512 1.29, 32768 x 512 1.62, 4096 x 1024
+    // 0.72, 4096 x 2048 0.68; M = 4: 1.00, 1.12, 1.74, 0.91, 0.67; e4m3, M = 1: 0.91,
+    // 1.29, 1.60, 1.00, 0.80.  (From N = 32768 on four are faster at K = 1024 too, 1.24, and
+    // one at 2048, 0.88.)  More activation rows: one where four would leave SMs without
+    // warps.  Measured, us, CUDA cores and tensor
     // cores: M = 1, int8, 512 x 512: 1.5 and 2.6, 512 x 2048 (K): 1.9 and 3.3, 8192 x
     // 8192: 12.2 and 14.0; M = 8, 4096 x 4096: 6.7 and 4.6; M = 80, 512 x 512: 2.4 and
     // 2.7, 2048 x 512: 5.5 and 2.8; e4m3, M = 1, 8192 x 8192: 17.1 and 14.1; M = 80,

@@ -4,7 +4,8 @@
 //
 //   s0 = max_k |v_k| / Q,   code_k = v_k / s0 rounded to nearest even
 //
-// (Q = 127 onto int8, the rule of rt_quantize_q8_row; Q = 448 onto FP8 E4M3).
+// (Q = 127 onto int8, the rule of rt_quantize_q8_row, s0 rounded to fp32; Q = 448
+// onto FP8 E4M3, s0 unrounded in the codes).
 //
 // Norm: y = h * rstd * g with rstd = 1 / sqrt(mean(h^2) + eps) > 0, so
 // y_k / max|y| = (h g)_k / max|h g|: the codes need only v = h * g, and rstd
@@ -12,10 +13,11 @@
 // therefore come from one pass over the row and one reduction, and no value
 // waits for rstd.
 //
-// A row stays in the registers of a group of TPR threads (NV vectors of 16
-// bytes a thread and input), so each input is read once and nothing is
-// written but the sum h, the codes and the scale.  Sums, maxima and values are
-// fp32.
+// A row stays with a group of TPR threads (NV vectors of 16 bytes a thread and
+// input), so each input is read once and nothing is written but the sum h, the
+// codes and the scale.  It stays in registers up to K = 16384 (fp32 norm and gate: 8192);
+// longer rows need more than the 64 that each of 1024 threads has, and the rest
+// is spilled (K = 32768: 2.4 to 5.7 TB/s).  Sums, maxima and values are fp32.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
