@@ -10,6 +10,9 @@ torch = pytest.importorskip("torch")
 import int8_dequant_gemm_b200 as rtq  # noqa: E402
 
 
+CURRENT = 5                                      # handle of the current stream
+
+
 class OnDevice(torch.Tensor):
     """A host tensor that says it is on cuda:0."""
     is_cuda = property(lambda self: True)
@@ -64,6 +67,7 @@ def world(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "stream", as_current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(CURRENT))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: Stream(handle))
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(rtq, "_lib", library)
@@ -105,7 +109,8 @@ def test_outputs_belong_to_the_stream_of_the_call(world, name, stream):
     assert seen == [stream.cuda_stream] * outputs
 
 
-def test_without_a_stream_they_come_from_the_current_one(world):
+@pytest.mark.parametrize("arguments", [{}, {"stream": Stream(CURRENT)}])
+def test_on_the_current_stream_they_come_from_it_as_it_is(world, arguments):
     for name in ("quantize_a8", "addnorm_a8", "gate_a8", "dequant_a8", "qgemm_a8"):
-        calls()[name][1]()
+        calls()[name][1](**arguments)
     assert world[1] == [None] * 9
