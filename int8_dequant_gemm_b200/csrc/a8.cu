@@ -777,11 +777,12 @@ cudaError_t launch_a8(const A8Plan &plan, const void *Xq, const float *xs, const
 // longer.  Time kept over time streamed, means of 2200 timings (M 12000 to 65536, N
 // 300 to 8192):
 //   K not a multiple of 64, by pieces of 128   2     3     4     5     7     8
-//     rows of Y whole, bf16, Y from 128 MB on 0.95  0.91  0.85  0.82  0.80  0.80
+//     Y of 128 MB and more, whole rows, bf16  0.95  0.91  0.85  0.82  0.80  0.80
 //     the same, fp32                          1.04  0.99  0.94  0.90  0.87  0.89
-//     ragged, bf16                            1.26  1.21  1.10  0.99  0.86  0.82
-//     ragged, fp32                            1.07  1.16  1.21  1.13  0.98  0.88
-//     Y within 128 MB, all four          0.95-1.12  0.88-1.07  0.88-1.00  0.88-0.98  ...
+//     ragged rows, bf16                       1.26  1.21  1.10  0.99  0.86  0.82
+//     ragged rows, fp32                       1.07  1.16  1.21  1.13  0.98  0.88
+//     Y below 128 MB, the worst of the four   1.12  1.07  1.00  0.98  0.97  0.97
+//     and the best                            0.95  0.88  0.88  0.88  0.88  0.85
 //   K an odd multiple of 64, 6 and 8 pieces: bf16 0.94 to 1.07, fp32 0.90 to 1.03 (ragged
 //     and large 1.22 and 1.05); 3 pieces 1.0 to 1.3, 9 0.9 to 1.1
 //   K a multiple of 128: 1.0 to 1.3, but for whole rows of N >= 4096, bf16 up to 6

@@ -112,14 +112,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8], const __half *) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 // |v| as bits: an order on magnitudes in which infinity is above every finite
 // value and NaN above infinity, so that one unsigned maximum finds both.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kTinyBits = 0x0D800000u;   // 2^-100: from here on 1 / (max / Q) is finite
 
 // max(mx, abs_bits(v)) in one instruction (any NaN becomes the NaN of all ones).
 __device__ __forceinline__ uint32_t max_bits(uint32_t mx, float v) {
@@ -127,8 +124,6 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t mx, float v) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(mx)), "f"(fabsf(v)));
     return __float_as_uint(m);
 }
-
-constexpr uint32_t kTinyBits = 0x0D800000u;   // 2^-100: from here on 1 / (max / Q) is finite
 
 // Unsigned maximum and (SUM) sum over the TPR threads of a row's group; every
 // thread gets both.  TPR > 32: through shared memory, `part` = one slot per
