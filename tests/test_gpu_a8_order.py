@@ -58,9 +58,12 @@ def turns(rtq, fmt, N, K, product, busy, want):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M,N,K,kernel", [
-    (1, 4096, 512, "simt"), (80, 4096, 512, "tc_w_stationary"), (300, 4096, 512, "tc_x_resident"),
-    (3000, 4096, 512, "tc_x_resident"), (300, 512, 2048, "tc_w_streamed"), (16384, 4096, 512, "tc_x_resident_pair")])
+KERNELS = [(1, 4096, 512, "simt"), (80, 4096, 512, "tc_w_stationary"), (300, 4096, 512, "tc_x_resident"),
+           (3000, 4096, 512, "tc_x_resident"), (300, 512, 2048, "tc_w_streamed"),
+           (16384, 4096, 512, "tc_x_resident_pair")]
+
+
+@pytest.mark.parametrize("M,N,K,kernel", KERNELS)
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
 def test_weight_only_products(rtq, busy, M, N, K, kernel, fmt):
     assert rtq.plan(fmt, M, N, K) == kernel
@@ -73,6 +76,36 @@ def test_weight_only_products(rtq, busy, M, N, K, kernel, fmt):
         return rtq.qgemm(fmt, x, c, s if fmt == Q8 else None, Y=out if out is not None else Y[next(turn)])
 
     turns(rtq, fmt, N, K, product, busy, lambda c, s: product(c, s, torch.empty(M, N, device="cuda")))
+
+
+@pytest.mark.parametrize("M,N,K,kernel", KERNELS)
+@pytest.mark.parametrize("fmt", [Q8, E4M3])
+def test_weight_only_products_captured(rtq, M, N, K, kernel, fmt):
+    """The same pair of launches twice in one graph, from two weights into one buffer of
+    codes, replayed back to back."""
+    assert rtq.plan(fmt, M, N, K) == kernel
+    x, ws = randn(M, K, seed=90), [randn(N, K, seed=i) for i in range(2)]
+    want = []
+    for w in ws:
+        c, s = rtq.quantize_a8(w, fmt)
+        torch.cuda.synchronize()
+        want.append(rtq.qgemm(fmt, x, c, s if fmt == Q8 else None))
+    Y = [torch.empty(M, N, device="cuda") for _ in ws]
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    rtq.workspace_reserve(rtq.workspace_bytes(fmt, M, N, K), stream=stream)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        for w, y in zip(ws, Y):
+            rtq.quantize_a8(w, fmt, codes=c, scales=s)
+            rtq.qgemm(fmt, x, c, s if fmt == Q8 else None, Y=y)
+    for _ in range(5):
+        for y in Y:
+            y.zero_()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        for y, v in zip(Y, want):
+            assert torch.equal(y, v)
 
 
 @pytest.mark.parametrize("fmt", [Q8, E4M3])
